@@ -3,8 +3,8 @@
 Operators: MXFP4 block quantisation and dequantisation of a frozen base
 (blocks of 32 E2M1 elements with one E8M0 scale), the frozen projection
 y = x W^T over MXFP4 weights with its input gradient dx = dy W, and the AdamW
-step over a group of tensors with states in 32 bits or in MXFP8 (E4M3
-elements, one E8M0 scale per 32).
+step over a group of tensors with states in 32 bits or in MXFP8 (E4M3 first
+and E5M2 second moments, one E8M0 scale per 32).
 
 ``run`` computes a case in plain torch operations (``own`` false) or through
 the library's calls (``own`` true) on what ``prepare`` made from the seed.
@@ -160,10 +160,15 @@ def _random16(index, tensor, seed, t):
     return torch.where((index & 1) == 1, h >> 16, h & 0xFFFF)
 
 
-def _block_scale(a):
-    """Scale exponents of blocks [n, 32] of magnitudes: the largest lands in [128, 256)."""
+# 8-bit states: element type, exponent that a block's largest element is brought to, mantissa bits, bias
+FORMATS = {"m": (torch.float8_e4m3fn, 7, 3, 7), "v": (torch.float8_e5m2, 14, 2, 15)}
+
+
+def _block_scale(a, top):
+    """Scale exponents of blocks [n, 32] of magnitudes: the largest lands in [2^top, 2^(top + 1))."""
     amax = a.amax(-1)
-    return torch.where(amax > 0, (_exponent(amax) - 7).clamp_min(-127), torch.full_like(amax, -127, dtype=torch.int32))
+    return torch.where(amax > 0, (_exponent(amax) - top).clamp_min(-127),
+                       torch.full_like(amax, -127, dtype=torch.int32))
 
 
 def _adamw(s):
@@ -173,15 +178,13 @@ def _adamw(s):
     lr, b1, b2, eps, wd = (f32(h[k]) for k in ("lr", "beta1", "beta2", "eps", "weight_decay"))
     g = s["grad"].float() * h["grad_scale"]
     if c["bits"] == 8:
-        m_old = s["m"].view(torch.float8_e4m3fn).float().view(-1, BLOCK) * _pow2(s["m_scale"].int() - 127)[:, None]
-        r_old = s["v"].view(torch.float8_e4m3fn).float().view(-1, BLOCK) * _pow2(s["v_scale"].int() - 127)[:, None]
-        m_old, v_old = m_old.view(-1), (r_old * r_old).view(-1)
+        m_old, v_old = ((s[k].view(FORMATS[k][0]).float().view(-1, BLOCK) *
+                         _pow2(s[k + "_scale"].int() - 127)[:, None]).view(-1) for k in ("m", "v"))
     else:
         m_old, v_old = s["m"], s["v"]
     m = m_old * b1 + g * f32(1.0 - b1)
     v = v_old * b2 + (g * g) * f32(1.0 - b2)
-    r = torch.sqrt(v)
-    denom = r * f32(1.0 / math.sqrt(1.0 - b2 ** t)) + eps
+    denom = torch.sqrt(v) * f32(1.0 / math.sqrt(1.0 - b2 ** t)) + eps
     theta = s["theta"] * f32(1.0 - lr * wd) - f32(lr / (1.0 - b1 ** t)) * (m / denom)
     s["theta"].copy_(theta)
     s["theta_bf16"].copy_(theta)
@@ -191,26 +194,29 @@ def _adamw(s):
         s["m"].copy_(m)
         s["v"].copy_(v)
         return
-    m, r = m.view(-1, BLOCK), r.view(-1, BLOCK)
-    em, er = _block_scale(m.abs()), _block_scale(r)
-    s["m"].copy_((m * _pow2(-em)[:, None]).to(torch.float8_e4m3fn).view(torch.uint8).view(-1))
-    y = r * _pow2(-er)[:, None]
-    low = y < 2.0 ** -6  # subnormal E4M3 values share the step of the first binade
-    z = torch.where(low, y + 2.0 ** -6, y)
-    bits = z.view(torch.int32) + (_random16(s["index"], s["tensor"], h["seed"], t) << 4).int().view(-1, BLOCK)
-    code = (bits >> 20) - 960 - torch.where(low, 8, 0)
-    code = torch.where((code == 0) & (r > 0), 1, code)
-    s["v"].copy_(code.to(torch.uint8).view(-1))
-    for e, name in ((em, "m_scale"), (er, "v_scale")):
-        s[name].copy_((e + 127).to(torch.uint8))
+    rnd = (_random16(s["index"], s["tensor"], h["seed"], t)).int().view(-1, BLOCK)
+    for x, name in ((m.view(-1, BLOCK), "m"), (v.view(-1, BLOCK), "v")):
+        _, top, mant, bias = FORMATS[name]
+        e = _block_scale(x.abs(), top)
+        y = x.abs() * _pow2(-e)[:, None]
+        least = 2.0 ** (1 - bias)  # below it elements are subnormal, with the step of the first binade
+        low = y < least
+        bits = torch.where(low, y + least, y).view(torch.int32) + (rnd << (23 - mant - 16))
+        code = (bits >> (23 - mant)) - ((127 - bias) << mant) - torch.where(low, 1 << mant, 0)
+        if name == "v":
+            code = torch.where((code == 0) & (x > 0), 1, code)
+        else:
+            code = code + torch.where(torch.signbit(x), 128, 0)
+        s[name].copy_(code.to(torch.uint8).view(-1))
+        s[name + "_scale"].copy_((e + 127).to(torch.uint8))
 
 
 def _adamw_outputs(s):
-    """The updated flat buffers; 8-bit states as the E4M3 elements and E8M0 scales that they are."""
+    """The updated flat buffers; 8-bit states as the elements and E8M0 scales that they are."""
     out = {k: s[k] for k in ("theta", "theta_bf16", "grad", "m", "v")}
     if s["case"]["bits"] == 8:
         for k in ("m", "v"):
-            out[k] = s[k].view(torch.float8_e4m3fn)
+            out[k] = s[k].view(FORMATS[k][0])
             out[k + "_scale"] = s[k + "_scale"].view(torch.float8_e8m0fnu)
     return out
 
@@ -286,10 +292,10 @@ def prepare(case, seed):
     if case["bits"] == 32:
         s["m"], s["v"] = m, r * r
     else:
-        for name, x in (("m", m), ("v", r)):
+        for name, x in (("m", m), ("v", r * r)):
             x = x.view(-1, BLOCK)
-            e = _block_scale(x.abs())
-            s[name] = (x * _pow2(-e)[:, None]).to(torch.float8_e4m3fn).view(torch.uint8).view(-1)
+            e = _block_scale(x.abs(), FORMATS[name][1])
+            s[name] = (x * _pow2(-e)[:, None]).to(FORMATS[name][0]).view(torch.uint8).view(-1)
             s[name + "_scale"] = (e + 127).to(torch.uint8)
         if not own:  # the counters of the plain form's random bits
             s["index"], s["tensor"] = index, tensor
@@ -386,7 +392,7 @@ def exact(case, seed):
     if case["bits"] == 8:
         per = lambda k: torch.exp2(s[k + "_scale"].double() - 127).repeat_interleave(BLOCK)  # noqa: E731
         m0 = s["m"].view(torch.float8_e4m3fn).double() * per("m")
-        v0 = (s["v"].view(torch.float8_e4m3fn).double() * per("v")) ** 2
+        v0 = s["v"].view(torch.float8_e5m2).double() * per("v")
     else:
         m0, v0 = s["m"].double(), s["v"].double()
     m, v = b1 * m0 + (1 - b1) * g, b2 * v0 + (1 - b2) * g * g
@@ -396,6 +402,6 @@ def exact(case, seed):
     got = {"theta": th, "theta_bf16": th, "grad": grad}
     if case["bits"] == 32:
         return got | {"m": m, "v": v}
-    # the 8-bit states' codes come from roundings of fp32 intermediates (and, for v, of random bits):
-    # they have no value of their own in 64 bits
+    # the 8-bit states' codes come from fp32 intermediates rounded by random bits: they have no value
+    # of their own in 64 bits
     return got | {"m": None, "v": None, "m_scale": None, "v_scale": None}
