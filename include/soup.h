@@ -9,11 +9,13 @@
  * backward pass re-reads and recomputes the layer and produces
  * dL/dx = W^T dL/dy plus the adapter terms, and dA, dB, while W stays frozen.
  *
- * Sections below: status and profiling; NF4 quantisation; the LoRA linear
- * layer; the decoder layer (forward, recompute backward, kept q|k|v); the
- * stream plan (slot ring, copies, waits); the disk tier (shard files read
- * ahead into staging buffers); layer blob layout; embedding, output head,
- * cross-entropy and DPO; SimPO and ORPO; the AdamW step on the adapters.
+ * Sections below: status and profiling; NF4 quantisation; MXFP4
+ * quantisation; the LoRA linear layer; the frozen linear layer; the decoder
+ * layer (forward, recompute backward, kept q|k|v); the stream plan (slot
+ * ring, copies, waits); the disk tier (shard files read ahead into staging
+ * buffers); layer blob layout; embedding, output head, cross-entropy and DPO;
+ * SimPO and ORPO; the AdamW step on the adapters; the AdamW step over a group
+ * of tensors, with states in 8 or 32 bits.
  *
  * Conventions for every entry point
  *  - Every function returns a soup_status; SOUP_OK (0) on success.  On failure
@@ -85,10 +87,10 @@ int64_t soup_launch_count(void);
  * in class_mask (bit c = class c) is bracketed by CUDA events recorded on its
  * own stream and tagged with its algorithmic work.  soup_profile_read
  * synchronises those events and sums them per class:
- * 0 = fused NF4-decode GEMM (forward, W), 1 = fused NF4-decode GEMM
- * (backward, W^T), 2 = other GEMMs with N > 64, 3 = skinny LoRA GEMMs
- * (N <= 64), 4 = fused NF4-decode GEMMs with a hi + lo A pair (either
- * direction), 5 = attention (forward and backward kernels; flops 4 B Hq d
+ * 0 = fused 4-bit-decode (NF4 or MXFP4) GEMM (forward, W), 1 = fused
+ * 4-bit-decode GEMM (backward, W^T), 2 = other GEMMs with N > 64, 3 = skinny
+ * LoRA GEMMs (N <= 64), 4 = fused 4-bit-decode GEMMs with a hi + lo A pair
+ * (either direction), 5 = attention (forward and backward kernels; flops 4 B Hq d
  * S(S+1)/2 forward, 2.5x that backward), 6 = RMSNorm forward / backward,
  * 7 = split-K reductions, 8 = other elementwise kernels (RoPE tables, LoRA
  * operand preparation, conversions, attention row dots, embedding gather),
@@ -129,6 +131,43 @@ soup_status soup_nf4_quantize(const float* W, int64_t out, int64_t in, uint8_t* 
 soup_status soup_nf4_dequant(const uint8_t* codes, const float* absmax, int64_t out,
                              int64_t in, uint16_t* W_bf16, void* stream);
 
+/* ---------------------------------------------------------------- MXFP4 ---
+ * A second 4-bit storage of the frozen base: MXFP4 of the OCP Microscaling
+ * Formats specification (v1.0), 4.25 bits per weight instead of NF4's 4.5.
+ * Blocks of 32 consecutive elements along the input dimension share one E8M0
+ * scale byte s, standing for 2^(s - 127) (255: NaN, the whole block is NaN);
+ * an element is E2M1 (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6).  Byte j of a row of codes holds element 2j in bits 3..0 and
+ * 2j + 1 in bits 7..4.  A row of scales has in / 32 bytes and is padded to
+ * soup_mx4_scale_stride(in) bytes (a multiple of 16; the padding is written
+ * as zeros by soup_mx4_quantize and read by nothing).
+ */
+#define SOUP_TYPE_F32 0
+#define SOUP_TYPE_BF16 1
+
+/* Bytes from one row of scales to the next: in / 32 rounded up to a multiple
+ * of 16 (0 for in <= 0). */
+int64_t soup_mx4_scale_stride(int64_t in);
+
+/* W [out, in] (w_type SOUP_TYPE_F32 or SOUP_TYPE_BF16, row stride ldw >= in
+ * elements) -> codes [out, in/2], scales [out, soup_mx4_scale_stride(in)].
+ * Per block with largest magnitude amax: e = max(floor(log2 amax) - 2, -127),
+ * s = e + 127, code = the E2M1 value nearest to w 2^-e, ties to even,
+ * saturating at 6; an all-zero block has s = 0.  A block with a NaN or an
+ * infinity gets s = 255 and codes 0, and *nonfinite_dev (optional device
+ * int32) is set to 1 (never cleared by the call).  W_bf16 (optional, [out,
+ * in] bf16): the stored values, as soup_mx4_dequant gives them.
+ * in: a positive multiple of 32; W, each of its rows, codes, scales and
+ * W_bf16 16-byte aligned.  One launch, asynchronous on `stream`. */
+soup_status soup_mx4_quantize(const void* W, int32_t w_type, int64_t out, int64_t in, int64_t ldw, uint8_t* codes,
+                              uint8_t* scales, uint16_t* W_bf16, int32_t* nonfinite_dev, void* stream);
+
+/* codes, scales -> W [out, in] bf16, exact (a value has two significant bits
+ * and at least 2^-128; one beyond bf16's largest, which the quantiser never
+ * stores, becomes infinite). */
+soup_status soup_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t out, int64_t in, uint16_t* W_bf16,
+                             void* stream);
+
 /* ----------------------------------------------------------- LoRA linear ---
  * One adapted projection, y = x W^T + s (x A^T) B^T with s = alpha/r
  * (row-vector form of y = W x + (alpha/r) B A x), W frozen.
@@ -140,20 +179,22 @@ soup_status soup_nf4_dequant(const uint8_t* codes, const float* absmax, int64_t 
  */
 #define SOUP_WEIGHT_NF4 0
 #define SOUP_WEIGHT_BF16 1
+#define SOUP_WEIGHT_MXFP4 2
 
 typedef struct soup_weight {
-  int32_t kind;          /* SOUP_WEIGHT_NF4 or SOUP_WEIGHT_BF16 */
+  int32_t kind;          /* SOUP_WEIGHT_NF4, SOUP_WEIGHT_BF16 or SOUP_WEIGHT_MXFP4 */
   int64_t out_features;  /* rows of W (N) */
-  int64_t in_features;   /* columns of W (K); a multiple of 64 */
-  const uint8_t* codes;  /* NF4: [out, in/2] */
+  int64_t in_features;   /* columns of W (K); a multiple of 64 (MXFP4: of 32) */
+  const uint8_t* codes;  /* NF4, MXFP4: [out, in/2] */
   const float* absmax;   /* NF4: [out, in/64] */
   const uint16_t* w;     /* BF16: [out, in] */
+  const uint8_t* scales; /* MXFP4: [out, soup_mx4_scale_stride(in)] */
 } soup_weight;
 
 /* Forward.  A [r, in] bf16, B [out, r] bf16 (r a multiple of 8, 8 <= r <= 64),
  * x [T, in] bf16, y [T, out] bf16, u_save [r, round_up(T, 8)] bf16.
- * T >= 1; out a multiple of 16; in a multiple of 64; all pointers 16-byte
- * aligned. */
+ * T >= 1; out a multiple of 16; in a multiple of 64 (MXFP4: of 32); all
+ * pointers 16-byte aligned. */
 soup_status soup_lora_linear_fwd(const soup_weight* W, const uint16_t* A, const uint16_t* B,
                                  int32_t r, float scale, const uint16_t* x, int64_t T,
                                  uint16_t* y, uint16_t* u_save, void* stream);
@@ -203,6 +244,24 @@ soup_status soup_lora_linear_bwd_noalloc(const soup_weight* W, const uint16_t* A
                                          int32_t r, float scale, const uint16_t* x,
                                          const uint16_t* u_save, const uint16_t* dy, int64_t T,
                                          uint16_t* dx, float* dA, float* dB, void* stream);
+
+/* --------------------------------------------------------- frozen linear ---
+ * The projection without adapters over any storage of W:
+ *   soup_linear_fwd   y [T, out] = x [T, in] W^T
+ *   soup_linear_bwd   dx [T, in] = dy [T, out] W     (W is frozen)
+ * x, y, dy, dx bf16 with row strides (elements) of at least the row, each a
+ * multiple of 8; fp32 accumulation, one rounding; out a multiple of 16, in of
+ * 64 (MXFP4: of 32); pointers 16-byte aligned.  T = 0 is a no-op; outputs
+ * beyond the row (between out and ldy) are left as they were.
+ * workspace (optional, 256-byte aligned, soup_linear_workspace(W, T) bytes;
+ * fewer or none is allowed and slower at some sizes): scratch of this call
+ * alone: calls that may overlap on the GPU need one each.  Its contents need
+ * no initialisation.  Asynchronous on `stream`; captures into graphs. */
+size_t soup_linear_workspace(const soup_weight* W, int64_t T);
+soup_status soup_linear_fwd(const soup_weight* W, const uint16_t* x, int64_t ldx, int64_t T, uint16_t* y, int64_t ldy,
+                            void* workspace, size_t workspace_bytes, void* stream);
+soup_status soup_linear_bwd(const soup_weight* W, const uint16_t* dy, int64_t lddy, int64_t T, uint16_t* dx,
+                            int64_t lddx, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------- attention ---
  * The decoder layer's causal GQA attention on its own (Soup pages, "how layer
@@ -274,7 +333,7 @@ typedef struct soup_layer_cfg {
   int32_t prefix_len;
 } soup_layer_cfg;
 
-/* The frozen base of one layer (all NF4 or all bf16), as it sits in a device
+/* The frozen base of one layer (all NF4, all MXFP4 or all bf16), as it sits in a device
  * slot.  Fused row layouts: qkv = [q; k; v] rows ([(Hq + 2 Hkv) d, H]),
  * gate_up = [gate; up] rows ([2 I, H]); o [H, Hq d]; down [H, I]. */
 typedef struct soup_layer_weights {
@@ -637,6 +696,61 @@ soup_status soup_adamw_step(float* theta, uint16_t* theta_bf16, float* grad, flo
                             float lr, float beta1, float beta2, float eps, float weight_decay,
                             float grad_scale, int64_t t, int32_t zero_grad, int32_t* nonfinite_dev,
                             void* stream);
+
+/* ---------------------------------------------------------- AdamW group ---
+ * The same AdamW step over many tensors in one launch, with the optimiser
+ * states in fp32 or in 8 bits (MXFP8 of the OCP Microscaling Formats
+ * specification: 8-bit elements, one E8M0 scale byte per block of 32).
+ *
+ * soup_adamw_tensor: n elements; theta fp32 master copy; theta_bf16 the bf16
+ * working copy or NULL; grad of the group's grad_type; m, v: fp32 [n]
+ * (state_bits 32), or uint8 [n] with m_scale, v_scale uint8 [ceil(n / 32)]
+ * (state_bits 8; all zeros is the state before the first step).  theta,
+ * theta_bf16, grad, m, v 16-byte aligned.  n = 0 is allowed.
+ *
+ * 8-bit states: m holds E4M3 codes and v E5M2 codes (sign bit 0): element i
+ * stands for element(code) 2^(scale[i / 32] - 127).  A step decodes them,
+ * forms the new m and v in fp32, updates theta from these unrounded values,
+ * and stores m and v rounded to one of their two neighbours by 16 random bits
+ * (a hash of seed, t, the tensor's place in the group and the element; equal
+ * arguments give equal bits), so that their means follow beta1 and beta2
+ * although one step moves them by less than a code.  A v above zero keeps a
+ * code above zero.  A state that is not finite is stored as NaN.  The block
+ * scale puts the largest finite element of m in [2^7, 2^8) and of v in
+ * [2^14, 2^15).
+ *
+ * soup_adamw_group_init checks the tensors (SOUP_ERR_INVALID_ARG when two
+ * buffers overlap), writes the group's tables to tables_dev
+ * (soup_adamw_group_bytes, 16-byte aligned, kept by the caller while the group
+ * is used), fills *group and SYNCHRONISES `stream`.  soup_adamw_group_step is
+ * one launch, asynchronous on `stream`; arguments as soup_adamw_step (t is
+ * taken when the call is made: a captured step replays that t).  Steps of one
+ * group must not overlap on the GPU. */
+typedef struct soup_adamw_tensor {
+  int64_t n;
+  float* theta;
+  uint16_t* theta_bf16;
+  void* grad;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+} soup_adamw_tensor;
+
+typedef struct soup_adamw_group {
+  void* tables; /* device */
+  size_t chunks_at;
+  int64_t n_chunks, n_elements;
+  int32_t n_tensors, state_bits, grad_type;
+} soup_adamw_group;
+
+size_t soup_adamw_group_bytes(const soup_adamw_tensor* tensors, int32_t n_tensors);
+soup_status soup_adamw_group_init(const soup_adamw_tensor* tensors, int32_t n_tensors, int32_t state_bits,
+                                  int32_t grad_type, void* tables_dev, size_t tables_bytes, soup_adamw_group* group,
+                                  void* stream);
+soup_status soup_adamw_group_step(const soup_adamw_group* group, float lr, float beta1, float beta2, float eps,
+                                  float weight_decay, float grad_scale, int64_t t, uint32_t seed, int32_t zero_grad,
+                                  int32_t* nonfinite_dev, void* stream);
 
 #ifdef __cplusplus
 }

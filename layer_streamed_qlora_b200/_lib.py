@@ -21,6 +21,8 @@ c_void_p, c_int32, c_int64, c_float, c_size_t = (ctypes.c_void_p, ctypes.c_int32
 
 SOUP_WEIGHT_NF4 = 0
 SOUP_WEIGHT_BF16 = 1
+SOUP_WEIGHT_MXFP4 = 2
+SOUP_TYPE_F32, SOUP_TYPE_BF16 = 0, 1
 
 
 class SoupError(RuntimeError):
@@ -31,7 +33,7 @@ class SoupError(RuntimeError):
 
 class SoupWeight(ctypes.Structure):
     _fields_ = [("kind", c_int32), ("out_features", c_int64), ("in_features", c_int64),
-                ("codes", c_void_p), ("absmax", c_void_p), ("w", c_void_p)]
+                ("codes", c_void_p), ("absmax", c_void_p), ("w", c_void_p), ("scales", c_void_p)]
 
 
 class LayerCfg(ctypes.Structure):
@@ -70,6 +72,16 @@ class DiskStats(ctypes.Structure):
                 ("read_ms", ctypes.c_double), ("wait_ms", ctypes.c_double), ("direct_files", c_int32)]
 
 
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("n", c_int64)] + [(k, c_void_p) for k in ("theta", "theta_bf16", "grad", "m", "v", "m_scale",
+                                                           "v_scale")]
+
+
+class AdamWGroupHandle(ctypes.Structure):
+    _fields_ = [("tables", c_void_p), ("chunks_at", c_size_t), ("n_chunks", c_int64), ("n_elements", c_int64),
+                ("n_tensors", c_int32), ("state_bits", c_int32), ("grad_type", c_int32)]
+
+
 SOUP_DISK_PINNED, SOUP_DISK_DIRECT = 1, 2
 
 
@@ -97,6 +109,20 @@ _SIGS = {
     "soup_profile_read": (c_int32, [ctypes.POINTER(GemmProfile), c_int32]),
     "soup_nf4_quantize": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p]),
     "soup_nf4_dequant": (c_int32, [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
+    "soup_mx4_scale_stride": (c_int64, [c_int64]),
+    "soup_mx4_quantize": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_void_p]),
+    "soup_mx4_dequant": (c_int32, [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
+    "soup_linear_workspace": (c_size_t, [ctypes.POINTER(SoupWeight), c_int64]),
+    "soup_linear_fwd": (c_int32, [ctypes.POINTER(SoupWeight), c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p,
+                                  c_size_t, c_void_p]),
+    "soup_linear_bwd": (c_int32, [ctypes.POINTER(SoupWeight), c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p,
+                                  c_size_t, c_void_p]),
+    "soup_adamw_group_bytes": (c_size_t, [ctypes.POINTER(AdamWTensor), c_int32]),
+    "soup_adamw_group_init": (c_int32, [ctypes.POINTER(AdamWTensor), c_int32, c_int32, c_int32, c_void_p, c_size_t,
+                                        ctypes.POINTER(AdamWGroupHandle), c_void_p]),
+    "soup_adamw_group_step": (c_int32, [ctypes.POINTER(AdamWGroupHandle), c_float, c_float, c_float, c_float, c_float,
+                                        c_float, c_int64, ctypes.c_uint32, c_int32, c_void_p, c_void_p]),
     "soup_lora_linear_fwd": (c_int32, [ctypes.POINTER(SoupWeight), c_void_p, c_void_p, c_int32, c_float,
                                        c_void_p, c_int64, c_void_p, c_void_p, c_void_p]),
     "soup_lora_linear_bwd_workspace": (c_size_t, [c_int64, c_int32, c_int64]),
@@ -289,6 +315,63 @@ def soup_nf4_dequant(codes, absmax, out_f, in_f, W_bf16, stream=None):
                                                       _stream(stream)))
 
 
+def _on_device(fn, dtype=None, **tensors):
+    """Refuses tensors that are not on the current CUDA device, not of `dtype`
+    (when given) or whose last dimension is not contiguous."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{fn}: {name} is {t.dtype}, not {dtype}")
+        if t.numel() > 1 and t.dim() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{fn}: {name}'s last dimension is not contiguous")
+
+
+def _whole(fn, n, **tensors):
+    """Refuses tensors that are not contiguous or hold fewer than n elements."""
+    for name, t in tensors.items():
+        if t is not None and (not t.is_contiguous() or t.numel() < n):
+            raise ValueError(f"{fn}: {name} must be contiguous with at least {n} elements, not {tuple(t.shape)}")
+
+
+# ---------------------------------------------------------------- MXFP4
+def soup_mx4_scale_stride(in_f) -> int:
+    """Bytes from one row of scales to the next: in_f / 32 rounded up to a multiple of 16."""
+    return int(lib().soup_mx4_scale_stride(int(in_f)))
+
+
+def soup_mx4_quantize(W, codes, scales, W_bf16=None, nonfinite=None, stream=None):
+    """W [out, in] fp32 or bf16 (rows may be strided) -> MXFP4 codes [out, in/2] and
+    scale bytes [out, soup_mx4_scale_stride(in)]; W_bf16 <- the stored values."""
+    fn = "soup_mx4_quantize"
+    if W.dim() != 2 or W.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{fn}: W must be a float32 or bfloat16 matrix, not {W.dtype} of shape {tuple(W.shape)}")
+    out_f, in_f = W.shape
+    _on_device(fn, W=W)
+    _on_device(fn, torch.uint8, codes=codes, scales=scales)
+    _on_device(fn, torch.bfloat16, W_bf16=W_bf16)
+    _on_device(fn, torch.int32, nonfinite=nonfinite)
+    _whole(fn, out_f * in_f // 2, codes=codes)
+    _whole(fn, out_f * soup_mx4_scale_stride(in_f), scales=scales)
+    _whole(fn, out_f * in_f, W_bf16=W_bf16)
+    _whole(fn, 1, nonfinite=nonfinite)
+    ldw = W.stride(0) if out_f > 1 else in_f
+    _check(fn, lib().soup_mx4_quantize(_p(W), SOUP_TYPE_F32 if W.dtype == torch.float32 else SOUP_TYPE_BF16, out_f,
+                                       in_f, ldw, _p(codes), _p(scales), _p(W_bf16), _p(nonfinite), _stream(stream)))
+
+
+def soup_mx4_dequant(codes, scales, out_f, in_f, W_bf16, stream=None):
+    fn = "soup_mx4_dequant"
+    _on_device(fn, torch.uint8, codes=codes, scales=scales)
+    _on_device(fn, torch.bfloat16, W_bf16=W_bf16)
+    _whole(fn, out_f * in_f // 2, codes=codes)
+    _whole(fn, out_f * soup_mx4_scale_stride(in_f), scales=scales)
+    _whole(fn, out_f * in_f, W_bf16=W_bf16)
+    _check(fn, lib().soup_mx4_dequant(_p(codes), _p(scales), out_f, in_f, _p(W_bf16), _stream(stream)))
+
+
 # ---------------------------------------------------------------- weights
 def weight_nf4(codes, absmax, out_f, in_f) -> SoupWeight:
     return SoupWeight(SOUP_WEIGHT_NF4, out_f, in_f, codes.data_ptr(), absmax.data_ptr(), None)
@@ -296,6 +379,96 @@ def weight_nf4(codes, absmax, out_f, in_f) -> SoupWeight:
 
 def weight_bf16(w) -> SoupWeight:
     return SoupWeight(SOUP_WEIGHT_BF16, w.shape[0], w.shape[1], None, None, w.data_ptr())
+
+
+def weight_mxfp4(codes, scales, out_f, in_f) -> SoupWeight:
+    return SoupWeight(SOUP_WEIGHT_MXFP4, out_f, in_f, codes.data_ptr(), None, None, scales.data_ptr())
+
+
+# ---------------------------------------------------------------- frozen linear
+def soup_linear_workspace(W: SoupWeight, T) -> int:
+    return int(lib().soup_linear_workspace(ctypes.byref(W), int(T)))
+
+
+def _linear(fn, W, a, a_cols, c, c_cols, workspace, stream):
+    for name, t, cols in (("input", a, a_cols), ("output", c, c_cols)):
+        if t.dim() != 2 or t.shape[1] != cols or t.shape[0] != a.shape[0]:
+            raise ValueError(f"{fn}: {name} must be [{a.shape[0]}, {cols}], not {tuple(t.shape)}")
+    _on_device(fn, torch.bfloat16, input=a, output=c)
+    _on_device(fn, workspace=workspace)
+    _whole(fn, 0, workspace=workspace)
+    T = a.shape[0]
+    lda, ldc = (t.stride(0) if T > 1 else cols for t, cols in ((a, a_cols), (c, c_cols)))
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(fn, getattr(lib(), fn)(ctypes.byref(W), _p(a), lda, T, _p(c), ldc, _p(workspace) if ws else None, ws,
+                                  _stream(stream)))
+
+
+def soup_linear_fwd(W: SoupWeight, x, y, workspace=None, stream=None):
+    """y [T, out] = x [T, in] W^T (bf16; rows may be strided)."""
+    _linear("soup_linear_fwd", W, x, W.in_features, y, W.out_features, workspace, stream)
+
+
+def soup_linear_bwd(W: SoupWeight, dy, dx, workspace=None, stream=None):
+    """dx [T, in] = dy [T, out] W (bf16; rows may be strided)."""
+    _linear("soup_linear_bwd", W, dy, W.out_features, dx, W.in_features, workspace, stream)
+
+
+# ---------------------------------------------------------------- AdamW group
+class AdamWGroup:
+    """AdamW over a list of tensors in one launch per step.
+
+    tensors: dicts with theta (fp32), grad (fp32 or bf16, the same for all),
+    m, v (fp32, or uint8 with m_scale, v_scale for state_bits=8) and optionally
+    theta_bf16; all contiguous and on the current device.  The group keeps
+    them alive."""
+
+    def __init__(self, tensors, state_bits=32, stream=None):
+        fn = "soup_adamw_group_init"
+        tensors = [dict(t) for t in tensors]
+        if not tensors:
+            raise ValueError(f"{fn}: no tensors")
+        state = torch.uint8 if state_bits == 8 else torch.float32
+        grad = tensors[0]["grad"].dtype
+        if grad not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"{fn}: gradients must be float32 or bfloat16, not {grad}")
+        arr = (AdamWTensor * len(tensors))()
+        for a, t in zip(arr, tensors):
+            n = t["theta"].numel()
+            _on_device(fn, torch.float32, theta=t["theta"])
+            _on_device(fn, torch.bfloat16, theta_bf16=t.get("theta_bf16"))
+            _on_device(fn, grad, grad=t["grad"])
+            _on_device(fn, state, m=t["m"], v=t["v"])
+            sc = {k: t[k] for k in ("m_scale", "v_scale")} if state_bits == 8 else {}
+            _on_device(fn, torch.uint8, **sc)
+            for k in ("theta", "theta_bf16", "grad", "m", "v"):
+                if t.get(k) is not None and (t[k].numel() != n or not t[k].is_contiguous()):
+                    raise ValueError(f"{fn}: {k} must be contiguous with theta's {n} elements")
+            _whole(fn, (n + 31) // 32, **sc)
+            a.n = n
+            if n:
+                for k in ("theta", "theta_bf16", "grad", "m", "v", *sc):
+                    setattr(a, k, t[k].data_ptr() if t.get(k) is not None else None)
+        self._tensors = tensors
+        self._handle = AdamWGroupHandle()
+        nbytes = lib().soup_adamw_group_bytes(arr, len(tensors))
+        self._tables = torch.empty(max(16, nbytes), dtype=torch.uint8, device="cuda")
+        _check(fn, lib().soup_adamw_group_init(arr, len(tensors), int(state_bits),
+                                               SOUP_TYPE_F32 if grad == torch.float32 else SOUP_TYPE_BF16,
+                                               _p(self._tables), self._tables.numel(), ctypes.byref(self._handle),
+                                               _stream(stream)))
+
+    def step(self, lr, beta1, beta2, eps, weight_decay, grad_scale, t, seed=0, zero_grad=False, nonfinite=None,
+             stream=None):
+        fn = "soup_adamw_group_step"
+        if self._tables.device.index != torch.cuda.current_device():
+            raise ValueError(f"{fn}: the group is on {self._tables.device}, not on the current CUDA device")
+        if nonfinite is not None:
+            _on_device(fn, torch.int32, nonfinite=nonfinite)
+            _whole(fn, 1, nonfinite=nonfinite)
+        _check(fn, lib().soup_adamw_group_step(ctypes.byref(self._handle), lr, beta1, beta2, eps, weight_decay,
+                                               grad_scale, int(t), int(seed) & 0xFFFFFFFF, 1 if zero_grad else 0,
+                                               _p(nonfinite), _stream(stream)))
 
 
 # ---------------------------------------------------------------- LoRA linear

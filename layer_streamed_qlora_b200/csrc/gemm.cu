@@ -30,6 +30,7 @@
 #include <atomic>
 
 #include "gemm.h"
+#include "mx4.cuh"
 #include "nf4_codebook.cuh"
 #include "ptx.cuh"
 #include "gscale.cuh"
@@ -42,17 +43,25 @@ constexpr int BM = 128;
 constexpr int BK = 64;
 constexpr int A_STAGE_BYTES = BM * BK * 2;  // 16 KB
 
-template <int BN, bool DUAL = false, int CG = 1, bool NF4B = true>
+// Classes of B operand: decoded from 4-bit codes by the decode warps (NF4 or
+// MXFP4) or brought by TMA in bf16; K-major (W) or MN-major (W^T).
+constexpr bool b_coded(int b) { return b >= B_NF4_K; }
+constexpr bool b_mx4(int b) { return b == B_MX4_K || b == B_MX4_MN; }
+constexpr bool b_mn(int b) { return b == B_TMA_MN || b == B_NF4_MN || b == B_MX4_MN; }
+
+template <int BN, bool DUAL = false, int CG = 1, bool NF4B = true, bool MX4 = false>
 struct Cfg {
   // DUAL: each stage holds two A tiles (the hi and lo bf16 parts of a more
   // precise A), multiplied against the same B tile.  CG = 2: the tile is
   // shared by a CTA pair (M = 256 over the pair, each CTA holds half of B).
   // NF4B (CTA pairs): B is decoded from NF4 codes; otherwise bf16 B tiles
-  // come straight from TMA and there is no decode table.
+  // come straight from TMA and there is no decode table.  MX4: the codes are
+  // MXFP4, decoded by arithmetic, so there is no table either.
   static constexpr int A_STAGE = A_STAGE_BYTES * (DUAL ? 2 : 1);
   static constexpr int B_STAGE = (BN / CG) * BK * 2;
   // NF4 CTA pairs also stage the packed codes (128 rows x 32 bytes, or 64
-  // k-rows x 64 bytes) and a 4-block-wide absmax box per stage through TMA
+  // k-rows x 64 bytes) and a 4-block-wide absmax box (MXFP4: 16 scale bytes
+  // per row) per stage through TMA
   static constexpr int C_STAGE = (CG == 2 && NF4B) ? 4096 : 0;
   static constexpr int S_STAGE = (CG == 2 && NF4B) ? 2048 : 0;
   static constexpr int TMEM_COLS = BN <= 32 ? 32 : (BN <= 64 ? 64 : (BN <= 128 ? 128 : 256));
@@ -61,7 +70,7 @@ struct Cfg {
   // x 16 half-warp lanes when two A tiles per stage leave no room) at the
   // start of shared memory; single CTAs: nibble table after the barriers
   static constexpr int LUT_LANES = DUAL ? 16 : 32;
-  static constexpr int LUT_BYTES = CG == 2 ? (NF4B ? 256 * LUT_LANES * 8 : 0) : 16 * 32 * 4;
+  static constexpr int LUT_BYTES = CG == 2 ? (NF4B && !MX4 ? 256 * LUT_LANES * 8 : 0) : 16 * 32 * 4;
   static constexpr int STAGE_BYTES = A_STAGE + B_STAGE + C_STAGE + S_STAGE;
   static constexpr int STAGE_BUDGET = CG == 2 ? (232448 - 1024 - BAR_BYTES - LUT_BYTES) : 196608;
   static constexpr int STAGES = (STAGE_BUDGET / STAGE_BYTES) > 8 ? 8 : (STAGE_BUDGET / STAGE_BYTES);
@@ -73,6 +82,8 @@ struct KArgs {
   int kb_split;  // split-K: k-blocks per slice (blockIdx.z = slice), 0 = no split
   const uint8_t* codes;
   const float* absmax;
+  const uint8_t* scales;  // MXFP4: scale bytes, rows of scale_stride
+  long long scale_stride;
   int tail_ksteps, nseg;
   int seg_end[4], seg_row[4];
   int pair_off;
@@ -239,6 +250,13 @@ __device__ __forceinline__ uint4 decode8_pairs(uint32_t w, const uint8_t* lut_by
     const float2 f = ptx::mul_f32x2(c, am);
     o[p] = pack_bf16x2(f.x, f.y);
   }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// 8 MXFP4 codes times their block's scale (2^(s - 127) as bf16x2).
+__device__ __forceinline__ uint4 decode8_mx4(uint32_t w, uint32_t scale2) {
+  uint32_t o[4];
+  mx4_decode8(w, scale2, o);
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -500,7 +518,7 @@ __device__ __forceinline__ void epilogue_tile(const KArgs& args, void* outp, uin
 }
 
 template <int BN, int AMJ, int BMD, bool TF, bool DUAL, int CG>
-__global__ void __launch_bounds__(32 * (2 + (BMD >= B_NF4_K ? 8 : 4)), 1)
+__global__ void __launch_bounds__(32 * (2 + (b_coded(BMD) ? 8 : 4)), 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmTA,
                 const __grid_constant__ CUtensorMap tmTB, const __grid_constant__ CUtensorMap tmA2,
@@ -508,10 +526,11 @@ __global__ void __launch_bounds__(32 * (2 + (BMD >= B_NF4_K ? 8 : 4)), 1)
                 const KArgs args) {
   using C = Cfg<BN, DUAL, CG>;
   static_assert(!DUAL || (AMJ == A_K && !TF), "dual-A: K-major bf16 A only");
-  static_assert(CG == 1 || (BN == 256 && AMJ == A_K && BMD >= B_NF4_K && !TF),
+  static_assert(CG == 1 || (BN == 256 && AMJ == A_K && b_coded(BMD) && !b_mx4(BMD) && !TF),
                 "CTA pairs: NF4 B, K-major bf16 A, 256-wide tiles");
-  constexpr bool NF4 = BMD >= B_NF4_K;
-  constexpr bool B_MN = (BMD == B_TMA_MN || BMD == B_NF4_MN);
+  static_assert(!b_mx4(BMD) || (BMD == B_MX4_K && BN == 128), "MXFP4 on one CTA: K-major 128-wide tiles");
+  constexpr bool NF4 = b_coded(BMD);
+  constexpr bool B_MN = b_mn(BMD);
   constexpr int STAGES = C::STAGES;
   constexpr int NEPI = NF4 ? 8 : 4;
   // Element geometry: every stage row is one 128-byte swizzle row.  bf16:
@@ -584,7 +603,7 @@ __global__ void __launch_bounds__(32 * (2 + (BMD >= B_NF4_K ? 8 : 4)), 1)
         const int b = i / C::LUT_LANES;
         lut2[i] = make_float2(__uint_as_float(c_nf4_bits[b >> 4]), __uint_as_float(c_nf4_bits[b & 15]));
       }
-    } else {
+    } else if constexpr (!b_mx4(BMD)) {
       for (int i = threadIdx.x - 64; i < 16 * 32; i += 256) lut[i] = __uint_as_float(c_nf4_bits[i >> 5]);
     }
   }
@@ -918,7 +937,50 @@ __global__ void __launch_bounds__(32 * (2 + (BMD >= B_NF4_K ? 8 : 4)), 1)
       // codes of stage it+1 are loaded into registers while stage it is
       // decoded, so the global-load latency overlaps the decode.
       const float* lut_lane = lut + lane;
-      if constexpr (BMD == B_NF4_K) {
+      if constexpr (BMD == B_MX4_K) {
+        // two threads per row, one block of 32 (one scale) each; the blocks
+        // of a last k-block that K ends inside are zeros
+        const int row = t >> 1, h = t & 1;
+        const int n = n0 + row;
+        const bool nvalid = n < args.N;
+        const uint8_t* src = args.codes + (size_t)(nvalid ? n : 0) * (args.K / 2) + h * 16;
+        const uint8_t* scp = args.scales + (size_t)(nvalid ? n : 0) * args.scale_stride + h;
+        uint32_t wn[4] = {0, 0, 0, 0};
+        uint32_t scn = 0;
+        if (nvalid && h * 32 < args.K) {
+          load_codes(src, wn);
+          scn = __ldg(scp);
+        }
+        for (int it = 0; it < n_iters; ++it) {
+          const int s = it % STAGES;
+          const uint32_t ph = (it / STAGES) & 1;
+          uint32_t w[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) w[u] = wn[u];
+          const uint32_t scale2 = mx4_scale_bf16x2(scn);
+          const bool valid = nvalid && it * BK + h * 32 < args.K;
+          if (nvalid && (it + 1) * BK + h * 32 < args.K) {
+            load_codes(src + (size_t)(it + 1) * 32, wn);
+            scn = __ldg(scp + (it + 1) * 2);
+          }
+          if (!ptx::mbar_wait_bounded(&empty[s], ph ^ 1, abort_flag, args.wait_limit)) {
+            atomicOr(args.err, 1);
+            *abort_flag = 1;
+            break;
+          }
+          if (it < num_kb) {
+            uint8_t* b = sB + s * C::B_STAGE;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint4 v = valid ? decode8_mx4(w[u], scale2) : make_uint4(0, 0, 0, 0);
+              st_shared_v4(b + row * 128 + (((h * 4 + u) ^ (row & 7)) << 4), v);
+            }
+            ptx::fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&full[s]);
+        }
+      } else if constexpr (BMD == B_NF4_K) {
         constexpr int TPR = 256 / BN;      // threads per row
         constexpr int EPT = 64 / TPR;      // elements per thread
         constexpr int NW = EPT / 8;        // 32-bit code words per thread
@@ -1105,9 +1167,10 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
                          const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmA3,
                          const KArgs args, int mtiles, int ntiles_total) {
   constexpr int BN = 256;
-  constexpr bool NF4 = BMD >= B_NF4_K;  // else bf16 B tiles by TMA, no decode
-  using C = Cfg<BN, DUAL, 2, NF4>;
-  constexpr bool B_MN = BMD == B_NF4_MN || BMD == B_TMA_MN;
+  constexpr bool NF4 = b_coded(BMD);  // else bf16 B tiles by TMA, no decode
+  constexpr bool MX4 = b_mx4(BMD);
+  using C = Cfg<BN, DUAL, 2, NF4, MX4>;
+  constexpr bool B_MN = b_mn(BMD);
   constexpr int STAGES = C::STAGES;
   constexpr int KSTEP_MN = 16 * 128;
   constexpr int CHUNK_BYTES = 64 * 128;
@@ -1164,7 +1227,7 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
       ptx::prefetch_tmap(&tmTB);
     }
   }
-  if (NF4 && warp >= 2 && warp < 10) {
+  if (NF4 && !MX4 && warp >= 2 && warp < 10) {
     float2* lut2 = reinterpret_cast<float2*>(smem_raw);
     for (int i = threadIdx.x - 64; i < 256 * C::LUT_LANES; i += 256) {
       const int b = i / C::LUT_LANES;
@@ -1226,19 +1289,22 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
             uint8_t* sc = sS + s * C::S_STAGE;
             const int ip = it + 12;
             ptx::mbar_arrive_expect_tx(&cfull[s], (uint32_t)(C::C_STAGE + (B_MN ? 1024 : 2048)));
+            // innermost coordinate of the absmax / scale box: 4 absmax of 64
+            // elements, or 16 scales of 32, from a multiple of 16 bytes
+            auto sbox = [](int e) { return MX4 ? (e / 32) & ~15 : (e / 64) & ~3; };
             if (!B_MN) {
               ptx::tma_load_2d(c, &tmB, &cfull[s], it * 32, r0);
-              ptx::tma_load_2d(sc, &tmA2, &cfull[s], it & ~3, r0);
+              ptx::tma_load_2d(sc, &tmA2, &cfull[s], sbox(it * BK), r0);
               if (ip < num_kb) {
                 ptx::tma_prefetch_l2_2d(&tmB, ip * 32, r0);
-                if ((ip & 3) == 0) ptx::tma_prefetch_l2_2d(&tmA2, ip, r0);
+                if ((ip & (MX4 ? 7 : 3)) == 0) ptx::tma_prefetch_l2_2d(&tmA2, sbox(ip * BK), r0);
               }
             } else {
               ptx::tma_load_2d(c, &tmB, &cfull[s], c0 / 2, it * BK);
-              ptx::tma_load_2d(sc, &tmA2, &cfull[s], (c0 / 64) & ~3, it * BK);
+              ptx::tma_load_2d(sc, &tmA2, &cfull[s], sbox(c0), it * BK);
               if (ip < num_kb) {
                 ptx::tma_prefetch_l2_2d(&tmB, c0 / 2, ip * BK);
-                ptx::tma_prefetch_l2_2d(&tmA2, (c0 / 64) & ~3, ip * BK);
+                ptx::tma_prefetch_l2_2d(&tmA2, sbox(c0), ip * BK);
               }
             }
           } else {
@@ -1333,7 +1399,7 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
       const int it_end = item_end(wi);
       int srow, unit0, chunk, coff, soff;
       bool valid;
-      if constexpr (BMD == B_NF4_K) {
+      if constexpr (!B_MN) {
         const int row = td >> 1, h = td & 1;
         const int n = paired ? (rank == 0 ? tl.nb + row : args.pair_off + tl.nb + row) : tl.n0 + (int)rank * 128 + row;
         valid = n < args.N;
@@ -1341,7 +1407,7 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
         unit0 = h * 4;
         chunk = 0;
         coff = row * 32 + h * 16;
-        soff = row * 4;
+        soff = MX4 ? row * 16 + h : row * 4;
       } else {
         const int q = td & 3, kr = td >> 2;
         const int col = tl.n0 + (int)rank * 128 + q * 32;
@@ -1350,7 +1416,8 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
         unit0 = (q & 1) * 4;
         chunk = q >> 1;
         coff = kr * 64 + q * 16;
-        soff = kr * 4 + ((tl.n0 + (int)rank * 128) / 64 & 3) + (q >> 1);
+        soff = MX4 ? kr * 16 + ((tl.n0 + (int)rank * 128) / 32 & 15) + q
+                   : kr * 4 + ((tl.n0 + (int)rank * 128) / 64 & 3) + (q >> 1);
       }
       uint8_t* const drow = sB + chunk * 8192 + srow * 128;
       for (int it = wi.kb0; it < it_end; ++it, ++gi) {
@@ -1366,14 +1433,25 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
         }
         if (it < num_kb) {
           const uint4 w = *reinterpret_cast<const uint4*>(sC + s * C::C_STAGE + coff);
-          const float am =
-              reinterpret_cast<const float*>(sS + s * C::S_STAGE)[soff + (BMD == B_NF4_K ? (it & 3) : 0)];
           uint8_t* b = drow + s * C::B_STAGE;
           const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+          if constexpr (MX4) {
+            // one block of 32 per thread; K-major: the blocks of a last
+            // k-block that K ends inside are zeros (their scale bytes are padding)
+            const uint32_t scale2 = mx4_scale_bf16x2(sS[s * C::S_STAGE + soff + (B_MN ? 0 : (it & 7) * 2)]);
+            const bool in_k = B_MN || it * BK + (unit0 >> 2) * 32 < args.K;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint4 v = valid ? decode8_pairs<C::LUT_LANES>(ws[u], lutb, lane_b, am) : make_uint4(0, 0, 0, 0);
-            st_shared_v4(b + (((unit0 + u) ^ (srow & 7)) << 4), v);
+            for (int u = 0; u < 4; ++u) {
+              const uint4 v = valid && in_k ? decode8_mx4(ws[u], scale2) : make_uint4(0, 0, 0, 0);
+              st_shared_v4(b + (((unit0 + u) ^ (srow & 7)) << 4), v);
+            }
+          } else {
+            const float am = reinterpret_cast<const float*>(sS + s * C::S_STAGE)[soff + (B_MN ? 0 : (it & 3))];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint4 v = valid ? decode8_pairs<C::LUT_LANES>(ws[u], lutb, lane_b, am) : make_uint4(0, 0, 0, 0);
+              st_shared_v4(b + (((unit0 + u) ^ (srow & 7)) << 4), v);
+            }
           }
           ptx::fence_proxy_async_smem();
         }
@@ -1565,23 +1643,24 @@ constexpr int CU_DT_U8 = 0;  // CU_TENSOR_MAP_DATA_TYPE_UINT8
 // epoch, so none ever needs clearing).
 constexpr int SK_MAX_TILES = 128;
 __device__ __align__(256) unsigned long long g_sk_cnt[2 * SK_MAX_TILES];
+static_assert(SK_COUNTER_BYTES == 2 * SK_MAX_TILES * sizeof(unsigned long long), "two counters per leftover tile");
 std::atomic<unsigned int> g_sk_epoch{0};
 
 // The split of the last partial round: leftover tiles L after the full
-// rounds on P pairs are cut into k slices (2 <= k <= 8, >= 64 k-blocks
+// rounds on P pairs are cut into k slices (2 <= k <= 8, >= min_kb k-blocks
 // each: a slice pays a pipeline fill, a 128 KB partial store per CTA and
 // its share of the sums) handed round-robin to the pairs; picked to
 // minimise the rounds the leftover then takes, ceil(L k / P) / k of a tile,
 // if that saves at least a tenth of a tile and the partials (L k x 256 KB)
 // fit the scratch.
-int pick_split(int total, int P, int num_kb, size_t scratch_bytes) {
+int pick_split(int total, int P, int num_kb, int min_kb, size_t scratch_bytes) {
   const int F = total / P, L = total - F * P;
   if (L == 0 || L > SK_MAX_TILES) return 0;
   int best = 0;
   double best_cost = 0.9;
   for (int k = 2; k <= 8; ++k) {
-    if (num_kb / k < 64) break;
-    if ((size_t)L * k * 2 * 256 * 128 * sizeof(float) > scratch_bytes) break;
+    if (num_kb / k < min_kb) break;
+    if ((size_t)L * k * SK_SLICE_BYTES > scratch_bytes) break;
     const double cost = (double)((L * k + P - 1) / P) / k + 0.01 * k;  // + a little per slice for the sums
     if (cost < best_cost) {
       best_cost = cost;
@@ -1591,10 +1670,13 @@ int pick_split(int total, int P, int num_kb, size_t scratch_bytes) {
   return best;
 }
 
+// Bytes of B per element as stored.
+constexpr double weight_bytes(int b) { return b_mx4(b) ? 0.5 + 1.0 / 32 : (b_coded(b) ? 0.5 + 4.0 / 64 : 2.0); }
+
 template <int BN, int AMJ, int BMD, bool TF = false, bool DUAL = false, int CG = 1, bool PERSIST = false>
 soup_status launch(const GemmDesc& d, const KArgs& ka, cudaStream_t st) {
   static_assert(!PERSIST || (CG == 2 && BN == 256 && AMJ == A_K && !TF), "persistent: CTA pairs, K-major A");
-  using C = Cfg<BN, DUAL, CG, (CG == 1 || BMD >= B_NF4_K)>;
+  using C = Cfg<BN, DUAL, CG, (CG == 1 || b_coded(BMD)), (CG == 2 && b_mx4(BMD))>;
   CUtensorMap mA, mB, mTA, mTB, mA2, mA3;
   memset(&mA2, 0, sizeof(mA2));
   memset(&mA3, 0, sizeof(mA3));
@@ -1607,12 +1689,18 @@ soup_status launch(const GemmDesc& d, const KArgs& ka, cudaStream_t st) {
   constexpr uint32_t EW = TF ? 32 : 64;  // elements per 128-byte row
   if (AMJ == A_K) SOUP_TRY(make_map(&mA, d.A, EW, 128, "A", TF));
   else SOUP_TRY(make_map(&mA, d.A, EW, EW, "A (MN-major)", TF, TF ? CU_SWIZZLE_128B_ATOM_32B : CU_SWIZZLE_128B));
-  constexpr bool B_MN = (BMD == B_TMA_MN || BMD == B_NF4_MN);
+  constexpr bool B_MN = b_mn(BMD);
   // K-major B boxes: the tile's rows (CTA pairs: this CTA's 128 of them;
   // paired gate|up tiles: one half of the pair's rows)
   if (BMD == B_TMA_K) SOUP_TRY(make_map(&mB, d.B, EW, CG == 2 ? 128 : (paired ? BN / 2 : BN), "B", TF));
   if (BMD == B_TMA_MN) SOUP_TRY(make_map(&mB, d.B, 64, 64, "B (MN-major)"));
-  if (CG == 2 && BMD >= B_NF4_K) {
+  if (CG == 2 && b_mx4(BMD)) {
+    // codes as below; 16 scale bytes per row
+    const int64_t rows = B_MN ? d.K : d.N, cols = B_MN ? d.N : d.K;
+    SOUP_TRY(make_plain_map(&mB, d.codes, rows, cols / 2, 1, CU_DT_U8, B_MN ? 64 : 32, B_MN ? 64 : 128, "MXFP4 codes"));
+    SOUP_TRY(make_plain_map(&mA2, d.scales, rows, mx4_scale_stride(cols), 1, CU_DT_U8, 16, B_MN ? 64 : 128,
+                            "MXFP4 scales"));
+  } else if (CG == 2 && b_coded(BMD)) {
     // codes and absmax staged per stage: K-major 128 rows x 32 bytes and a
     // 128 x 4 absmax box; transposed 64 k-rows x 64 bytes and a 64 x 4 box
     if (BMD == B_NF4_K) {
@@ -1662,27 +1750,29 @@ soup_status launch(const GemmDesc& d, const KArgs& ka, cudaStream_t st) {
     KArgs kx = ka;
     kx.sk_k = 0;
     if (d.sk_scratch && d.sk_scratch_bytes > 0 && soup_aligned(d.sk_scratch, 16)) {
-      const int k = pick_split(total, max_pairs, ka.num_kb, d.sk_scratch_bytes);
+      const int k = pick_split(total, max_pairs, ka.num_kb, d.sk_min_kb, d.sk_scratch_bytes);
       if (k >= 2) {
-        void* cnt = nullptr;
-        SOUP_TRY(static_symbol_address(SYM_SPLIT_COUNTERS, reinterpret_cast<const void*>(g_sk_cnt), &cnt));
+        void* cnt = d.sk_counters;
+        if (cnt)
+          SOUP_CUDA_TRY(cudaMemsetAsync(cnt, 0, SK_COUNTER_BYTES, st));
+        else
+          SOUP_TRY(static_symbol_address(SYM_SPLIT_COUNTERS, reinterpret_cast<const void*>(g_sk_cnt), &cnt));
         const int F = total / max_pairs;
         kx.sk_full = F;
         kx.sk_units = (total - F * max_pairs) * k;
         kx.sk_k = k;
         kx.sk_ws = static_cast<float*>(d.sk_scratch);
         kx.sk_cnt = static_cast<unsigned long long*>(cnt);
-        kx.sk_epoch = g_sk_epoch.fetch_add(1) + 1;
+        kx.sk_epoch = d.sk_counters ? 1u : g_sk_epoch.fetch_add(1) + 1;
         npairs = F > 0 ? max_pairs : std::min(kx.sk_units, max_pairs);
       }
     }
     cfg.gridDim = dim3(2 * npairs);
     if (profiling()) {
-      const int cls = BMD < B_NF4_K ? GC_BF16
-                                    : (DUAL ? GC_NF4_DUAL : (BMD == B_NF4_K ? GC_NF4_FWD : GC_NF4_BWD));
+      const int cls = !b_coded(BMD) ? GC_BF16 : (DUAL ? GC_NF4_DUAL : (!B_MN ? GC_NF4_FWD : GC_NF4_BWD));
       const double tail_k = d.tail_ksteps > 0 ? (double)d.tailA.rows : 0.0;
       const double flops = 2.0 * d.M * d.N * ((double)d.K * (DUAL ? 2 : 1) + (paired ? 16.0 : tail_k));
-      const double wbytes = BMD >= B_NF4_K ? (double)d.N * d.K * (0.5 + 4.0 / 64) : (double)d.N * d.K * 2;
+      const double wbytes = (double)d.N * d.K * weight_bytes(BMD);
       const double bytes = (double)d.M * d.K * 2 + wbytes +
                            (double)d.M * d.N * ((d.out_kind == OUT_F32 || d.out_kind == OUT_F32_T) ? 4 : 2);
       profile_begin(st, cls, flops, bytes);
@@ -1698,18 +1788,18 @@ soup_status launch(const GemmDesc& d, const KArgs& ka, cudaStream_t st) {
     SOUP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
     attr_set = true;
   }
-  constexpr int NT = 32 * (2 + (BMD >= B_NF4_K ? 8 : 4));
+  constexpr int NT = 32 * (2 + (b_coded(BMD) ? 8 : 4));
   const int ntiles = paired ? (d.pair_off + BN / 2 - 1) / (BN / 2) : (d.N + BN - 1) / BN;
   const int nz = ka.kb_split > 0 ? (ka.num_kb + ka.kb_split - 1) / ka.kb_split : 1;
   dim3 grid(CG == 2 ? 2 * ((d.M + 2 * BM - 1) / (2 * BM)) : (d.M + BM - 1) / BM, ntiles, nz);
   if (profiling()) {
     // algorithmic work: 2 M N K (+ 2 M N r for the LoRA tail); bytes: the
     // operands read once and the output written once
-    const int cls = (DUAL && BMD >= B_NF4_K) ? GC_NF4_DUAL
-                    : BMD == B_NF4_K ? GC_NF4_FWD : (BMD == B_NF4_MN ? GC_NF4_BWD : (d.N <= 64 ? GC_SKINNY : GC_BF16));
+    const int cls = b_coded(BMD) ? (DUAL ? GC_NF4_DUAL : (!B_MN ? GC_NF4_FWD : GC_NF4_BWD))
+                                 : (d.N <= 64 ? GC_SKINNY : GC_BF16);
     const double tail_k = d.tail_ksteps > 0 ? (double)d.tailA.rows : 0.0;
     const double flops = 2.0 * d.M * d.N * ((double)d.K * (DUAL ? 2 : 1) + (paired ? 16.0 : tail_k));
-    const double wbytes = (BMD >= B_NF4_K) ? (double)d.N * d.K * (0.5 + 4.0 / 64) : (double)d.N * d.K * 2;
+    const double wbytes = (double)d.N * d.K * weight_bytes(BMD);
     const int oes = (d.out_kind == OUT_F32 || d.out_kind == OUT_F32_T) ? 4 : 2;
     const double bytes = (double)d.M * d.K * 2 + wbytes + (double)d.M * d.N * oes;
     profile_begin(st, cls, flops, bytes);
@@ -1740,14 +1830,16 @@ soup_status launch(const GemmDesc& d, const KArgs& ka, cudaStream_t st) {
 
 int pick_bn(const GemmDesc& d) {
   if (d.bn) return d.bn;
-  const bool nf4 = d.b_mode >= B_NF4_K;
-  const bool mn = d.b_mode == B_TMA_MN || d.b_mode == B_NF4_MN;
+  const bool nf4 = b_coded(d.b_mode);
+  const bool mn = b_mn(d.b_mode);
   auto fits = [&](int bn) {
     for (int i = 0; i < d.nseg - 1; ++i)
       if (d.seg_end[i] % bn) return false;
     return true;
   };
   if (d.pair_off > 0) return 256;
+  // MXFP4: CTA pairs (256-wide tiles) unless an N segment ends inside one
+  if (b_mx4(d.b_mode)) return fits(256) ? 256 : 128;
   if (!nf4 && !mn && d.N <= 64) return ((d.N + 15) / 16) * 16;
   if (d.N >= 256 && (d.N % 256 == 0 || d.N >= 1024) && fits(256)) return 256;
   if (d.N >= 128 && fits(128)) return 128;
@@ -1756,7 +1848,21 @@ int pick_bn(const GemmDesc& d) {
 
 // Kernel selection for one launch (after the descriptor checks).
 soup_status dispatch(const GemmDesc& d, const KArgs& ka, int bn, cudaStream_t st) {
-  const bool nf4 = d.b_mode >= B_NF4_K;
+  if (b_mx4(d.b_mode)) {
+    const bool dual = d.A_lo.ptr != nullptr, mn = d.b_mode == B_MX4_MN;
+    SOUP_CHECK(!dual || (d.A_lo.rows == d.A.rows && d.A_lo.cols == d.A.cols), SOUP_ERR_SHAPE,
+               "gemm: hi and lo parts of A differ in shape");
+    if (bn == 256 && !mn)
+      return dual ? launch<256, A_K, B_MX4_K, false, true, 2, true>(d, ka, st)
+                  : launch<256, A_K, B_MX4_K, false, false, 2, true>(d, ka, st);
+    if (bn == 256)
+      return dual ? launch<256, A_K, B_MX4_MN, false, true, 2, true>(d, ka, st)
+                  : launch<256, A_K, B_MX4_MN, false, false, 2, true>(d, ka, st);
+    if (bn == 128 && !mn)
+      return dual ? launch<128, A_K, B_MX4_K, false, true>(d, ka, st) : launch<128, A_K, B_MX4_K>(d, ka, st);
+    return fail(SOUP_ERR_SHAPE, "gemm: no MXFP4 kernel for BN=%d b_mode=%d", bn, d.b_mode);
+  }
+  const bool nf4 = b_coded(d.b_mode);
   if (d.tf32) {
     SOUP_CHECK(d.b_mode == B_TMA_K && d.tail_ksteps == 0 && d.pair_off == 0 && d.epi == EPI_STORE && bn <= 64,
                SOUP_ERR_SHAPE, "gemm: tf32 mode supports skinny (N <= 64) K-major-B GEMMs without tail");
@@ -1843,12 +1949,21 @@ soup_status gemm(const GemmDesc& d, cudaStream_t st) {
   SOUP_CHECK(d.out != nullptr, SOUP_ERR_INVALID_ARG, "gemm: null output");
   SOUP_CHECK(d.tail_ksteps >= 0 && d.tail_ksteps <= 4, SOUP_ERR_SHAPE, "gemm: tail_ksteps %d", d.tail_ksteps);
   SOUP_CHECK(d.nseg >= 1 && d.nseg <= 4, SOUP_ERR_SHAPE, "gemm: nseg %d", d.nseg);
-  const bool nf4 = d.b_mode >= B_NF4_K;
-  if (nf4) {
+  const bool nf4 = b_coded(d.b_mode);
+  if (b_mx4(d.b_mode)) {
+    SOUP_CHECK(d.codes && d.scales, SOUP_ERR_INVALID_ARG, "gemm: MXFP4 operand missing");
+    SOUP_CHECK(d.a_major == A_K && !d.tf32, SOUP_ERR_SHAPE, "gemm: MXFP4 B needs a K-major bf16 A");
+    SOUP_CHECK((d.b_mode == B_MX4_K ? d.K : d.N) % 32 == 0, SOUP_ERR_SHAPE,
+               "gemm: MXFP4 needs rows of a multiple of 32 elements");
+    SOUP_CHECK(soup_aligned(d.codes, 16) && soup_aligned(d.scales, 16), SOUP_ERR_ALIGN,
+               "gemm: MXFP4 codes or scales not 16-byte aligned");
+  } else if (nf4) {
     SOUP_CHECK(d.codes && d.absmax, SOUP_ERR_INVALID_ARG, "gemm: NF4 operand missing");
     SOUP_CHECK(d.a_major == A_K, SOUP_ERR_SHAPE, "gemm: NF4 B needs a K-major A");
-    SOUP_CHECK(d.K % 64 == 0, SOUP_ERR_SHAPE, "gemm: NF4 needs K %% 64 == 0 (K=%d)", d.K);
-    if (d.b_mode == B_NF4_MN)
+    // transposed, K is W's row count: rows beyond it are zeros in both operands
+    if (d.b_mode == B_NF4_K)
+      SOUP_CHECK(d.K % 64 == 0, SOUP_ERR_SHAPE, "gemm: NF4 needs K %% 64 == 0 (K=%d)", d.K);
+    else
       SOUP_CHECK(d.N % 64 == 0, SOUP_ERR_SHAPE, "gemm: NF4 (transposed) needs N %% 64 == 0");
     SOUP_CHECK(soup_aligned(d.codes, 16), SOUP_ERR_ALIGN, "gemm: NF4 codes misaligned");
   }
@@ -1858,7 +1973,7 @@ soup_status gemm(const GemmDesc& d, cudaStream_t st) {
                d.seg_end[i], bn);
   if (d.pair_off > 0) {
     SOUP_CHECK(d.N == 2 * d.pair_off && d.pair_off % 128 == 0 && bn == 256 &&
-                   (d.b_mode == B_NF4_K || d.b_mode == B_TMA_K) && d.a_major == A_K,
+                   (d.b_mode == B_NF4_K || d.b_mode == B_TMA_K || d.b_mode == B_MX4_K) && d.a_major == A_K,
                SOUP_ERR_SHAPE, "gemm: paired tiles need N = 2*pair_off, pair_off %% 128 == 0, K-major B");
     SOUP_CHECK(d.tail_ksteps == 0 || d.tail_ksteps == 1, SOUP_ERR_SHAPE, "gemm: paired tiles take one tail step per half");
   }
@@ -1873,7 +1988,8 @@ soup_status gemm(const GemmDesc& d, cudaStream_t st) {
   memset(&ka, 0, sizeof(ka));
   ka.M = d.M; ka.N = d.N; ka.K = d.K;
   ka.num_kb = d.tf32 ? (d.K + 31) / 32 : (d.K + BK - 1) / BK;
-  ka.codes = d.codes; ka.absmax = d.absmax;
+  ka.codes = d.codes; ka.absmax = d.absmax; ka.scales = d.scales;
+  if (b_mx4(d.b_mode)) ka.scale_stride = mx4_scale_stride(d.b_mode == B_MX4_K ? d.K : d.N);
   ka.tail_ksteps = d.tail_ksteps; ka.nseg = d.nseg;
   for (int i = 0; i < 4; ++i) { ka.seg_end[i] = d.seg_end[i]; ka.seg_row[i] = d.seg_row[i]; }
   ka.pair_off = d.pair_off;

@@ -24,6 +24,8 @@ enum BMode : int {
   B_TMA_MN = 1,  // B stored [K, N] bf16
   B_NF4_K = 2,   // B = dequant(codes [N, K/2], absmax [N, K/64])      (forward W)
   B_NF4_MN = 3,  // B = dequant(codes [K, N/2], absmax [K, N/64])^T    (backward W^T)
+  B_MX4_K = 4,   // B = dequant(codes [N, K/2], scales [N, stride(K)])   (MXFP4, forward W)
+  B_MX4_MN = 5,  // B = dequant(codes [K, N/2], scales [K, stride(N)])^T (MXFP4, backward W^T)
 };
 // Output element type and layout: row-major [M, N] or transposed [N, M].
 enum OutKind : int { OUT_BF16 = 0, OUT_BF16_T = 1, OUT_F32 = 2, OUT_F32_T = 3, OUT_F16 = 4 };
@@ -48,7 +50,8 @@ struct GemmDesc {
   int b_mode = B_TMA_K;
   Mat B;                    // bf16 B for TMA modes
   const uint8_t* codes = nullptr;
-  const float* absmax = nullptr;
+  const float* absmax = nullptr;   // NF4
+  const uint8_t* scales = nullptr;  // MXFP4: rows of mx4_scale_stride bytes
   // Optional extra K-block appended after the main loop ("tail"): a LoRA
   // up-projection folded into the same accumulator.  tailA is stored
   // transposed, [rows, M] (row offset chosen per N segment), tailB has the
@@ -103,6 +106,12 @@ struct GemmDesc {
   // that nothing else uses during the call.
   void* sk_scratch = nullptr;
   size_t sk_scratch_bytes = 0;
+  // least k-blocks of a slice of that split
+  int sk_min_kb = 64;
+  // The split's slice counters (SK_COUNTER_BYTES, cleared on the stream
+  // before the launch), for callers whose launches may overlap on the GPU or
+  // be replayed from a graph; null: the library's, tagged per launch.
+  unsigned long long* sk_counters = nullptr;
   // Optional split-K for skinny GEMMs (N <= 64, TMA operands, plain store
   // epilogue): when a workspace is given and the M x N tiles alone cannot
   // fill the GPU, the K range is cut into up to 8 slices whose fp32 partial
@@ -117,6 +126,9 @@ struct GemmDesc {
   // no loads and never arrives, so the MMA warp's bounded wait runs out.
   int debug_skip_producer = 0;
 };
+
+constexpr size_t SK_COUNTER_BYTES = 2048;  // 2 counters for each of at most 128 leftover tiles
+constexpr size_t SK_SLICE_BYTES = 2 * 256 * 128 * sizeof(float);
 
 soup_status gemm(const GemmDesc& d, cudaStream_t stream);
 

@@ -804,7 +804,8 @@ extern "C" soup_status soup_layer_blob_views(const soup_layer_cfg* cfg, int32_t 
   Dims m;
   SOUP_TRY(make_dims(&one, 1, 1, &m));
   SOUP_CHECK(out, SOUP_ERR_INVALID_ARG, "soup_layer_blob_views: null out");
-  SOUP_CHECK(kind == SOUP_WEIGHT_NF4 || kind == SOUP_WEIGHT_BF16, SOUP_ERR_INVALID_ARG, "bad weight kind %d", kind);
+  SOUP_CHECK(kind == SOUP_WEIGHT_NF4 || kind == SOUP_WEIGHT_BF16 || kind == SOUP_WEIGHT_MXFP4, SOUP_ERR_INVALID_ARG,
+             "bad weight kind %d", kind);
   SOUP_CHECK(soup_aligned(base, 256), SOUP_ERR_ALIGN, "soup_layer_blob_views: base not 256-byte aligned");
   const char* b = static_cast<const char*>(base);
   size_t o = 0;
@@ -822,6 +823,11 @@ extern "C" soup_status soup_layer_blob_views(const soup_layer_cfg* cfg, int32_t 
       o += align256(n / 2);
       w.absmax = reinterpret_cast<const float*>(b + o);
       o += align256(n / 64 * 4);
+    } else if (kind == SOUP_WEIGHT_MXFP4) {
+      w.codes = reinterpret_cast<const uint8_t*>(b + o);
+      o += align256(n / 2);
+      w.scales = reinterpret_cast<const uint8_t*>(b + o);
+      o += align256((size_t)parts[i].out * soup_mx4_scale_stride(parts[i].in));
     } else {
       w.w = reinterpret_cast<const uint16_t*>(b + o);
       o += align256(n * 2);

@@ -1,0 +1,81 @@
+// The frozen projection without adapters: y = x W^T and its input gradient
+// dx = dy W (W is frozen, so there is no weight gradient), on the tcgen05
+// GEMM engine, for every storage of W.
+//
+// The engine's 256 x 256 tiles leave most of the GPU idle when T is a few
+// hundred tokens; with a workspace the tiles that do not fill a round are cut
+// along K (slices of at least 8 k-blocks), summed in slice order.
+#include <algorithm>
+
+#include "gemm.h"
+#include "lora_internal.h"
+
+namespace soup {
+namespace {
+
+constexpr int64_t MAX_SLICES = 148;  // two per CTA pair: 37 MiB of partials at most
+
+size_t workspace_bytes_for(int64_t M, int64_t N) {
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  return SK_COUNTER_BYTES + (size_t)std::min<int64_t>(tiles * 8, MAX_SLICES) * SK_SLICE_BYTES;
+}
+
+soup_status check_linear(const char* fn, const soup_weight* W, const void* a, int64_t lda, int64_t a_cols, int64_t T,
+                         const void* c, int64_t ldc, int64_t c_cols, const void* ws, size_t ws_bytes) {
+  SOUP_TRY(check_weight(W, fn));
+  SOUP_CHECK(T >= 0 && T < (1 << 30), SOUP_ERR_SHAPE, "%s: T=%lld", fn, (long long)T);
+  if (T == 0) return SOUP_OK;
+  SOUP_CHECK(a && c, SOUP_ERR_INVALID_ARG, "%s: null pointer", fn);
+  SOUP_CHECK(lda >= a_cols && ldc >= c_cols, SOUP_ERR_SHAPE, "%s: a row stride is less than the row", fn);
+  SOUP_CHECK(soup_aligned(a, 16) && soup_aligned(c, 16) && lda % 8 == 0 && ldc % 8 == 0, SOUP_ERR_ALIGN,
+             "%s: rows of x, y, dy and dx must be 16-byte aligned", fn);
+  SOUP_CHECK(!ws_bytes || (ws && soup_aligned(ws, 256)), SOUP_ERR_ALIGN, "%s: workspace null or not 256-byte aligned",
+             fn);
+  return SOUP_OK;
+}
+
+void use_workspace(GemmDesc& g, void* ws, size_t bytes) {
+  if (!ws || bytes < SK_COUNTER_BYTES + 2 * SK_SLICE_BYTES) return;
+  g.sk_counters = static_cast<unsigned long long*>(ws);
+  g.sk_scratch = static_cast<char*>(ws) + SK_COUNTER_BYTES;
+  g.sk_scratch_bytes = std::min(bytes - SK_COUNTER_BYTES, (size_t)MAX_SLICES * SK_SLICE_BYTES);
+  g.sk_min_kb = 8;
+}
+
+}  // namespace
+}  // namespace soup
+
+using namespace soup;
+
+extern "C" size_t soup_linear_workspace(const soup_weight* W, int64_t T) {
+  if (!W || T <= 0 || W->out_features <= 0 || W->in_features <= 0) return 0;
+  return std::max(workspace_bytes_for(T, W->out_features), workspace_bytes_for(T, W->in_features));
+}
+
+extern "C" soup_status soup_linear_fwd(const soup_weight* W, const uint16_t* x, int64_t ldx, int64_t T, uint16_t* y,
+                                       int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  SOUP_TRY(check_linear("soup_linear_fwd", W, x, ldx, W ? W->in_features : 0, T, y, ldy, W ? W->out_features : 0,
+                        workspace, workspace_bytes));
+  if (T == 0) return SOUP_OK;
+  GemmDesc g;
+  g.M = (int)T; g.N = (int)W->out_features; g.K = (int)W->in_features;
+  g.A = Mat{x, T, W->in_features, ldx};
+  set_weight_fwd(g, W);
+  g.out_kind = OUT_BF16; g.out = y; g.ldo = ldy;
+  use_workspace(g, workspace, workspace_bytes);
+  return gemm(g, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" soup_status soup_linear_bwd(const soup_weight* W, const uint16_t* dy, int64_t lddy, int64_t T, uint16_t* dx,
+                                       int64_t lddx, void* workspace, size_t workspace_bytes, void* stream) {
+  SOUP_TRY(check_linear("soup_linear_bwd", W, dy, lddy, W ? W->out_features : 0, T, dx, lddx, W ? W->in_features : 0,
+                        workspace, workspace_bytes));
+  if (T == 0) return SOUP_OK;
+  GemmDesc g;
+  g.M = (int)T; g.N = (int)W->in_features; g.K = (int)W->out_features;
+  g.A = Mat{dy, T, W->out_features, lddy};
+  set_weight_bwd(g, W);
+  g.out_kind = OUT_BF16; g.out = dx; g.ldo = lddx;
+  use_workspace(g, workspace, workspace_bytes);
+  return gemm(g, static_cast<cudaStream_t>(stream));
+}

@@ -47,16 +47,21 @@ soup_status transpose_bf16(const uint16_t* in, int rows, int cols, uint16_t* out
 
 soup_status check_weight(const soup_weight* W, const char* fn) {
   SOUP_CHECK(W, SOUP_ERR_INVALID_ARG, "%s: null weight", fn);
-  SOUP_CHECK(W->kind == SOUP_WEIGHT_NF4 || W->kind == SOUP_WEIGHT_BF16, SOUP_ERR_INVALID_ARG,
-             "%s: unknown weight kind %d", fn, W->kind);
-  SOUP_CHECK(W->out_features > 0 && W->in_features > 0 && W->in_features % 64 == 0 &&
+  SOUP_CHECK(W->kind == SOUP_WEIGHT_NF4 || W->kind == SOUP_WEIGHT_BF16 || W->kind == SOUP_WEIGHT_MXFP4,
+             SOUP_ERR_INVALID_ARG, "%s: unknown weight kind %d", fn, W->kind);
+  const int in_mult = W->kind == SOUP_WEIGHT_MXFP4 ? 32 : 64;
+  SOUP_CHECK(W->out_features > 0 && W->in_features > 0 && W->in_features % in_mult == 0 &&
                  W->out_features % 16 == 0 && W->out_features < (1 << 30) && W->in_features < (1 << 30),
-             SOUP_ERR_SHAPE, "%s: W must be [out, in] with out %% 16 == 0 and in %% 64 == 0 (got %lld x %lld)",
-             fn, (long long)W->out_features, (long long)W->in_features);
+             SOUP_ERR_SHAPE, "%s: W must be [out, in] with out %% 16 == 0 and in %% %d == 0 (got %lld x %lld)",
+             fn, in_mult, (long long)W->out_features, (long long)W->in_features);
   if (W->kind == SOUP_WEIGHT_NF4) {
     SOUP_CHECK(W->codes && W->absmax, SOUP_ERR_INVALID_ARG, "%s: NF4 weight without codes/absmax", fn);
     SOUP_CHECK(soup_aligned(W->codes, 16) && soup_aligned(W->absmax, 4), SOUP_ERR_ALIGN,
                "%s: NF4 codes must be 16-byte aligned", fn);
+  } else if (W->kind == SOUP_WEIGHT_MXFP4) {
+    SOUP_CHECK(W->codes && W->scales, SOUP_ERR_INVALID_ARG, "%s: MXFP4 weight without codes/scales", fn);
+    SOUP_CHECK(soup_aligned(W->codes, 16) && soup_aligned(W->scales, 16), SOUP_ERR_ALIGN,
+               "%s: MXFP4 codes and scales must be 16-byte aligned", fn);
   } else {
     SOUP_CHECK(W->w && soup_aligned(W->w, 16), SOUP_ERR_ALIGN, "%s: bf16 weight null or misaligned", fn);
   }
@@ -70,6 +75,10 @@ void set_weight_fwd(GemmDesc& g, const soup_weight* W) {
     g.b_mode = B_NF4_K;
     g.codes = W->codes;
     g.absmax = W->absmax;
+  } else if (W->kind == SOUP_WEIGHT_MXFP4) {
+    g.b_mode = B_MX4_K;
+    g.codes = W->codes;
+    g.scales = W->scales;
   } else {
     g.b_mode = B_TMA_K;
     g.B = Mat{W->w, W->out_features, W->in_features, W->in_features};
@@ -81,6 +90,10 @@ void set_weight_bwd(GemmDesc& g, const soup_weight* W) {
     g.b_mode = B_NF4_MN;
     g.codes = W->codes;
     g.absmax = W->absmax;
+  } else if (W->kind == SOUP_WEIGHT_MXFP4) {
+    g.b_mode = B_MX4_MN;
+    g.codes = W->codes;
+    g.scales = W->scales;
   } else {
     g.b_mode = B_TMA_MN;
     g.B = Mat{W->w, W->out_features, W->in_features, W->in_features};

@@ -1,0 +1,346 @@
+// AdamW over a group of tensors in one launch, optimiser states in fp32 or in
+// MXFP8 (8-bit elements, one E8M0 scale byte per block of 32): E4M3 for m,
+// E5M2 for v, whose range is squared.
+//
+// The update is that of optim.cu.  With 8-bit states a step decodes m and v
+// of each element, forms the new ones in fp32, updates theta from these, and
+// stores them again, each rounded to one of its two neighbours at random with
+// the probability that keeps the mean.  Rounded to nearest neither would
+// follow its average: a step moves v by a part 1 - beta2 (1e-3) of itself and
+// m by 1 - beta1 (0.1) of its distance from the gradient, while half a code
+// step is 6 to 12 % of v and 3 to 6 % of m: v would never fall, and m would
+// stop at two thirds of a constant gradient.  A v above zero keeps at least
+// the smallest code, so m / sqrt(v) has no zero divisor that the fp32 state
+// would not have.
+// The block's scale brings the largest element to [2^7, 2^8) (E4M3) or
+// [2^14, 2^15) (E5M2), below the largest value even after rounding up;
+// elements of m down to 2^-17 and of v down to 2^-31 of it have a code.  An
+// element that is not finite is stored as NaN and does not take part in the
+// maximum.
+//
+// The random bits are a hash of (seed, step, tensor, element), so a step gives
+// the same bits on every run and with any launch shape; m and v of an element
+// share them (each rounding is unbiased by itself, and m / sqrt(v) errs less
+// when both go the same way).
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <exception>
+#include <vector>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "soup_internal.h"
+
+namespace soup {
+namespace {
+
+constexpr int CHUNK = 2048;  // elements per CTA turn: 256 threads x 8
+
+// Device tables of a group: GroupTensor[n_tensors], then GroupChunk[n_chunks].
+struct GroupTensor {
+  int64_t n;
+  float* theta;
+  uint16_t* theta_bf16;
+  void* grad;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+};
+struct GroupChunk {
+  uint32_t tensor, chunk;
+};
+
+struct GroupArgs {
+  const GroupTensor* tensors;
+  const GroupChunk* chunks;
+  int64_t n_chunks;
+  float decay, beta1, one_minus_beta1, beta2, one_minus_beta2, step_size, inv_sqrt_bc2, eps, grad_scale;
+  int zero_grad;
+  uint32_t seed, t;
+  int32_t* nonfinite;
+};
+
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+
+// A bijective 32-bit mix (xor-shifts and odd multipliers, Appleby 2011).
+__device__ __forceinline__ uint32_t mix32(uint32_t h) {
+  h ^= h >> 16;
+  h *= 0x85EBCA6Bu;
+  h ^= h >> 13;
+  h *= 0xC2B2AE35u;
+  return h ^ (h >> 16);
+}
+
+__device__ __forceinline__ float e8m0(uint32_t s) { return __uint_as_float(s ? s << 23 : 1u << 22); }
+
+// The two element formats: MANT mantissa bits, exponent bias, and the
+// exponent TOP that a block's largest element is brought to.
+struct E4M3 {
+  static constexpr uint32_t MANT = 3, BIAS = 7, TOP = 7;
+};
+struct E5M2 {
+  static constexpr uint32_t MANT = 2, BIAS = 15, TOP = 14;
+};
+
+// Scale byte of a block whose largest magnitude has the bits `top`, and the
+// factor 2^(127 - s) that brings the block to the format's range.
+template <class F>
+__device__ __forceinline__ uint32_t block_scale(uint32_t top, float& up) {
+  const uint32_t E = top >> 23, s = E > F::TOP ? E - F::TOP : 0u;
+  up = __uint_as_float((254u - s) << 23);
+  return s;
+}
+
+__device__ __forceinline__ float e4m3_to_f32(uint32_t c) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3)));
+}
+// E5M2 is the upper byte of an fp16.
+__device__ __forceinline__ float e5m2_to_f32(uint32_t c) { return __half2float(__ushort_as_half((uint16_t)(c << 8))); }
+
+// Magnitude code of y in [0, 2^(TOP + 1)), the dropped mantissa bits rounded
+// by 16 random bits at their top.  Below 2^(1 - BIAS) elements are subnormal
+// with the step of the first binade, so 2^(1 - BIAS) is added and the codes
+// of one binade taken off again.
+template <class F>
+__device__ __forceinline__ uint32_t encode_stochastic(float y, uint32_t rnd16) {
+  constexpr float LEAST = 1.f / (1u << (F::BIAS - 1));
+  constexpr uint32_t ZERO = (127 - F::BIAS) << F::MANT;
+  const bool low = y < LEAST;
+  const uint32_t bits = __float_as_uint(low ? y + LEAST : y) + (rnd16 << (23 - F::MANT - 16));
+  return (bits >> (23 - F::MANT)) - (low ? ZERO + (1u << F::MANT) : ZERO);
+}
+
+__device__ __forceinline__ float new_m(const GroupArgs& a, float m, float g) {
+  return __fadd_rn(__fmul_rn(m, a.beta1), __fmul_rn(g, a.one_minus_beta1));
+}
+__device__ __forceinline__ float new_v(const GroupArgs& a, float v, float g) {
+  return __fadd_rn(__fmul_rn(v, a.beta2), __fmul_rn(__fmul_rn(g, g), a.one_minus_beta2));
+}
+
+template <bool G16>
+__device__ __forceinline__ float load_grad(const void* grad, int64_t i) {
+  if (G16) return __bfloat162float(static_cast<const __nv_bfloat16*>(grad)[i]);
+  return static_cast<const float*>(grad)[i];
+}
+
+template <int BITS, bool G16>
+__global__ void __launch_bounds__(256) adamw_group_kernel(const GroupArgs a) {
+  bool bad = false;
+  for (int64_t c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
+    const GroupChunk ch = a.chunks[c];
+    const GroupTensor& t = a.tensors[ch.tensor];
+    const int64_t i0 = (int64_t)ch.chunk * CHUNK;
+    const uint32_t key = mix32(mix32(ch.tensor + 0x9E3779B9u * a.t) + a.seed);
+    // element e of a block of 32 is lane e: a warp takes 8 blocks in turn
+    for (int k = 0; k < CHUNK / 256; ++k) {
+      const int64_t i = i0 + k * 256 + threadIdx.x;
+      const bool in_range = i < t.n;
+      float g = 0.f, m = 0.f, v = 0.f, p = 0.f;
+      if (in_range) {
+        const float g_raw = load_grad<G16>(t.grad, i);
+        bad |= !finite(g_raw);
+        g = g_raw * a.grad_scale;
+        p = t.theta[i];
+        if (BITS == 32) {
+          m = static_cast<const float*>(t.m)[i];
+          v = static_cast<const float*>(t.v)[i];
+        } else {
+          m = e4m3_to_f32(static_cast<const uint8_t*>(t.m)[i]) * e8m0(t.m_scale[i >> 5]);
+          v = e5m2_to_f32(static_cast<const uint8_t*>(t.v)[i]) * e8m0(t.v_scale[i >> 5]);
+        }
+      }
+      m = new_m(a, m, g);
+      v = new_v(a, v, g);
+      const float r = __fsqrt_rn(v);
+      if (in_range) {
+        p = __fsub_rn(__fmul_rn(p, a.decay),
+                      __fmul_rn(a.step_size, __fdiv_rn(m, __fadd_rn(__fmul_rn(r, a.inv_sqrt_bc2), a.eps))));
+        t.theta[i] = p;
+        if (t.theta_bf16) reinterpret_cast<__nv_bfloat16*>(t.theta_bf16)[i] = __float2bfloat16_rn(p);
+        if (a.zero_grad) {
+          if (G16) static_cast<uint16_t*>(t.grad)[i] = 0;
+          else static_cast<float*>(t.grad)[i] = 0.f;
+        }
+        if (BITS == 32) {
+          static_cast<float*>(t.m)[i] = m;
+          static_cast<float*>(t.v)[i] = v;
+        }
+      }
+      if (BITS == 8) {
+        uint32_t tm = in_range && finite(m) ? __float_as_uint(m) & 0x7FFFFFFFu : 0u;
+        uint32_t tv = in_range && finite(v) ? __float_as_uint(v) : 0u;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          tm = max(tm, __shfl_xor_sync(0xFFFFFFFFu, tm, o));
+          tv = max(tv, __shfl_xor_sync(0xFFFFFFFFu, tv, o));
+        }
+        float um, uv;
+        const uint32_t sm = block_scale<E4M3>(tm, um), sv = block_scale<E5M2>(tv, uv);
+        if (in_range) {
+          const uint32_t h = mix32((uint32_t)(i >> 1) + key);
+          const uint32_t rnd = (i & 1) ? h >> 16 : h & 0xFFFFu;
+          uint32_t cm = encode_stochastic<E4M3>(fabsf(m) * um, rnd) | (__float_as_uint(m) >> 31 << 7);
+          if (!finite(m)) cm = 0x7F;
+          uint32_t cv = encode_stochastic<E5M2>(v * uv, rnd);
+          if (cv == 0 && v > 0.f) cv = 1;
+          if (!finite(v)) cv = 0x7F;
+          static_cast<uint8_t*>(t.m)[i] = (uint8_t)cm;
+          static_cast<uint8_t*>(t.v)[i] = (uint8_t)cv;
+          if ((i & 31) == 0) {
+            t.m_scale[i >> 5] = (uint8_t)sm;
+            t.v_scale[i >> 5] = (uint8_t)sv;
+          }
+        }
+      }
+    }
+  }
+  if (bad && a.nonfinite) *a.nonfinite = 1;
+}
+
+size_t align16(size_t v) { return (v + 15) / 16 * 16; }
+
+int64_t chunks_of(int64_t n) { return (n + CHUNK - 1) / CHUNK; }
+
+}  // namespace
+}  // namespace soup
+
+using namespace soup;
+
+extern "C" size_t soup_adamw_group_bytes(const soup_adamw_tensor* tensors, int32_t n_tensors) {
+  if (!tensors || n_tensors <= 0) return 0;
+  int64_t chunks = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) chunks += tensors[i].n > 0 ? chunks_of(tensors[i].n) : 0;
+  return align16((size_t)n_tensors * sizeof(GroupTensor)) + (size_t)chunks * sizeof(GroupChunk);
+}
+
+extern "C" soup_status soup_adamw_group_init(const soup_adamw_tensor* tensors, int32_t n_tensors, int32_t state_bits,
+                                             int32_t grad_type, void* tables_dev, size_t tables_bytes,
+                                             soup_adamw_group* group, void* stream) {
+  const char* fn = "soup_adamw_group_init";
+  SOUP_CHECK(tensors && group, SOUP_ERR_INVALID_ARG, "%s: null pointer", fn);
+  SOUP_CHECK(n_tensors >= 1, SOUP_ERR_SHAPE, "%s: n_tensors %d", fn, n_tensors);
+  SOUP_CHECK(state_bits == 8 || state_bits == 32, SOUP_ERR_INVALID_ARG, "%s: state_bits %d is neither 8 nor 32", fn,
+             state_bits);
+  SOUP_CHECK(grad_type == SOUP_TYPE_F32 || grad_type == SOUP_TYPE_BF16, SOUP_ERR_INVALID_ARG,
+             "%s: grad_type %d is neither SOUP_TYPE_F32 nor SOUP_TYPE_BF16", fn, grad_type);
+  try {
+    std::vector<GroupTensor> gt(n_tensors);
+    std::vector<GroupChunk> gc;
+    int64_t total = 0;
+    struct Range {
+      const char *lo, *hi;
+      int32_t tensor;
+    };
+    std::vector<Range> ranges;
+    for (int32_t i = 0; i < n_tensors; ++i) {
+      const soup_adamw_tensor& s = tensors[i];
+      SOUP_CHECK(s.n >= 0 && s.n < (1ll << 40), SOUP_ERR_SHAPE, "%s: tensor %d has n = %lld", fn, i, (long long)s.n);
+      memset(&gt[i], 0, sizeof(gt[i]));
+      if (s.n == 0) continue;
+      SOUP_CHECK(s.theta && s.grad && s.m && s.v && (state_bits == 32 || (s.m_scale && s.v_scale)),
+                 SOUP_ERR_INVALID_ARG, "%s: tensor %d has a null pointer", fn, i);
+      SOUP_CHECK(soup_aligned(s.theta, 16) && soup_aligned(s.theta_bf16, 16) && soup_aligned(s.grad, 16) &&
+                     soup_aligned(s.m, 16) && soup_aligned(s.v, 16),
+                 SOUP_ERR_ALIGN, "%s: tensor %d: theta, theta_bf16, grad, m and v must be 16-byte aligned", fn, i);
+      gt[i] = GroupTensor{s.n, s.theta, s.theta_bf16, s.grad, s.m, s.v, s.m_scale, s.v_scale};
+      for (int64_t c = 0; c < chunks_of(s.n); ++c) gc.push_back(GroupChunk{(uint32_t)i, (uint32_t)c});
+      total += s.n;
+      const size_t gs = grad_type == SOUP_TYPE_F32 ? 4 : 2, ss = state_bits / 8;
+      auto add = [&](const void* p, size_t bytes) {
+        if (p) ranges.push_back(Range{static_cast<const char*>(p), static_cast<const char*>(p) + bytes, i});
+      };
+      add(s.theta, s.n * 4);
+      add(s.theta_bf16, s.n * 2);
+      add(s.grad, s.n * gs);
+      add(s.m, s.n * ss);
+      add(s.v, s.n * ss);
+      if (state_bits == 8) {
+        add(s.m_scale, (s.n + 31) / 32);
+        add(s.v_scale, (s.n + 31) / 32);
+      }
+    }
+    // every buffer is written by the step: none may share memory with another
+    std::sort(ranges.begin(), ranges.end(), [](const Range& x, const Range& y) { return x.lo < y.lo; });
+    for (size_t k = 1; k < ranges.size(); ++k)
+      SOUP_CHECK(ranges[k].lo >= ranges[k - 1].hi, SOUP_ERR_INVALID_ARG,
+                 "%s: buffers of tensors %d and %d overlap", fn, ranges[k - 1].tensor, ranges[k].tensor);
+    const size_t need = soup_adamw_group_bytes(tensors, n_tensors);
+    SOUP_CHECK(tables_dev && tables_bytes >= need, SOUP_ERR_INVALID_ARG, "%s: %zu bytes of tables, %zu needed", fn,
+               tables_bytes, need);
+    SOUP_CHECK(soup_aligned(tables_dev, 16), SOUP_ERR_ALIGN, "%s: tables not 16-byte aligned", fn);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    char* base = static_cast<char*>(tables_dev);
+    const size_t chunks_at = align16(gt.size() * sizeof(GroupTensor));
+    SOUP_CUDA_TRY(cudaMemcpyAsync(base, gt.data(), gt.size() * sizeof(GroupTensor), cudaMemcpyHostToDevice, st));
+    if (!gc.empty())
+      SOUP_CUDA_TRY(
+          cudaMemcpyAsync(base + chunks_at, gc.data(), gc.size() * sizeof(GroupChunk), cudaMemcpyHostToDevice, st));
+    SOUP_CUDA_TRY(cudaStreamSynchronize(st));
+    group->tables = base;
+    group->chunks_at = chunks_at;
+    group->n_chunks = (int64_t)gc.size();
+    group->n_elements = total;
+    group->n_tensors = n_tensors;
+    group->state_bits = state_bits;
+    group->grad_type = grad_type;
+  } catch (const std::exception& e) {
+    return fail(SOUP_ERR_INVALID_ARG, "%s: host memory: %s", fn, e.what());
+  }
+  return SOUP_OK;
+}
+
+extern "C" soup_status soup_adamw_group_step(const soup_adamw_group* group, float lr, float beta1, float beta2,
+                                             float eps, float weight_decay, float grad_scale, int64_t t, uint32_t seed,
+                                             int32_t zero_grad, int32_t* nonfinite_dev, void* stream) {
+  const char* fn = "soup_adamw_group_step";
+  SOUP_CHECK(group && group->tables && group->n_chunks >= 0, SOUP_ERR_INVALID_ARG, "%s: group not initialised", fn);
+  SOUP_CHECK((group->state_bits == 8 || group->state_bits == 32) &&
+                 (group->grad_type == SOUP_TYPE_F32 || group->grad_type == SOUP_TYPE_BF16),
+             SOUP_ERR_INVALID_ARG, "%s: group not initialised", fn);
+  SOUP_CHECK(t >= 1, SOUP_ERR_INVALID_ARG, "%s: the step index t starts at 1", fn);
+  SOUP_CHECK(beta1 >= 0.f && beta1 < 1.f && beta2 >= 0.f && beta2 < 1.f && eps > 0.f && lr >= 0.f &&
+                 weight_decay >= 0.f,
+             SOUP_ERR_INVALID_ARG, "%s: need 0 <= beta < 1, eps > 0, lr >= 0, weight_decay >= 0", fn);
+  if (group->n_chunks == 0) return SOUP_OK;
+  // bias corrections in double on the host
+  const double bc1 = 1.0 - std::pow((double)beta1, (double)t);
+  const double bc2 = 1.0 - std::pow((double)beta2, (double)t);
+  const char* base = static_cast<const char*>(group->tables);
+  GroupArgs a;
+  a.tensors = reinterpret_cast<const GroupTensor*>(base);
+  a.chunks = reinterpret_cast<const GroupChunk*>(base + group->chunks_at);
+  a.n_chunks = group->n_chunks;
+  a.decay = (float)(1.0 - (double)lr * (double)weight_decay);
+  a.beta1 = beta1;
+  a.one_minus_beta1 = (float)(1.0 - (double)beta1);
+  a.beta2 = beta2;
+  a.one_minus_beta2 = (float)(1.0 - (double)beta2);
+  a.step_size = (float)((double)lr / bc1);
+  a.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(bc2));
+  a.eps = eps;
+  a.grad_scale = grad_scale;
+  a.zero_grad = zero_grad ? 1 : 0;
+  a.seed = seed;
+  a.t = (uint32_t)t;
+  a.nonfinite = nonfinite_dev;
+  const bool g16 = group->grad_type == SOUP_TYPE_BF16;
+  const unsigned grid = (unsigned)std::min<int64_t>(group->n_chunks, (int64_t)sm_count() * 8);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const double gb = g16 ? 2 : 4;
+  profile_begin(st, GC_ADAMW, 0.0,
+                (double)group->n_elements * (10.0 + gb * (zero_grad ? 2 : 1) + (group->state_bits == 32 ? 16.0 : 4.125)));
+  if (group->state_bits == 32) {
+    if (g16) adamw_group_kernel<32, true><<<grid, 256, 0, st>>>(a);
+    else adamw_group_kernel<32, false><<<grid, 256, 0, st>>>(a);
+  } else {
+    if (g16) adamw_group_kernel<8, true><<<grid, 256, 0, st>>>(a);
+    else adamw_group_kernel<8, false><<<grid, 256, 0, st>>>(a);
+  }
+  SOUP_LAUNCH_CHECK();
+  profile_end(st);
+  return SOUP_OK;
+}

@@ -1,4 +1,4 @@
-"""Layer-streamed LoRA training step over a frozen NF4 (or bf16) base.
+"""Layer-streamed LoRA training step over a frozen NF4 (or MXFP4, or bf16) base.
 
 The Soup pages' method ("how layer streaming works"): the frozen base is cut
 into per-layer shards held in pinned host RAM; a ring of `stream_buffers`
@@ -47,7 +47,7 @@ class ModelConfig:
     n_layers: int
     eps: float = 1e-5
     theta: float = 5e5
-    kind: str = "nf4"      # "nf4" or "bf16" frozen base
+    kind: str = "nf4"      # "nf4", "mxfp4" or "bf16" frozen base
     tied: bool = False     # lm_head == embed_tokens
 
     @property
@@ -67,7 +67,7 @@ class ModelConfig:
 
     @property
     def weight_kind(self):
-        return L.SOUP_WEIGHT_NF4 if self.kind == "nf4" else L.SOUP_WEIGHT_BF16
+        return {"nf4": L.SOUP_WEIGHT_NF4, "mxfp4": L.SOUP_WEIGHT_MXFP4}.get(self.kind, L.SOUP_WEIGHT_BF16)
 
 
 def _seed(*parts) -> int:
@@ -121,12 +121,18 @@ class SyntheticWeights:
 class AdamW:
     """AdamW hyperparameters for the adapters.  The Soup pages' run sets only
     the learning rate (5e-4); the rest are the defaults of the Trainer those
-    pages run on (betas 0.9 / 0.999, eps 1e-8, no weight decay)."""
+    pages run on (betas 0.9 / 0.999, eps 1e-8, no weight decay).
+
+    state_bits: 32 holds the two moments in fp32 (8 bytes per parameter), 8 in
+    MXFP8 (2.06 bytes; see soup_adamw_group_step), whose random rounding draws
+    from `seed`."""
     lr: float = 5e-4
     beta1: float = 0.9
     beta2: float = 0.999
     eps: float = 1e-8
     weight_decay: float = 0.0
+    state_bits: int = 32
+    seed: int = 0
 
 
 def token_rows(batch: int, seq: int, prompt_share: int = 0) -> int:
@@ -277,6 +283,8 @@ class StreamedLoRAModel:
         self.stream_recompute = stream_recompute
         self.disk = None
         self.adamw = adamw or AdamW()
+        if self.adamw.state_bits not in (8, 32):
+            raise ValueError(f"AdamW.state_bits must be 8 or 32, not {self.adamw.state_bits!r}")
         if task not in ("sft", "dpo", "simpo", "orpo"):
             raise ValueError(f"task must be 'sft', 'dpo', 'simpo' or 'orpo', not {task!r}")
         self.task = task
@@ -388,6 +396,13 @@ class StreamedLoRAModel:
                                                     L.c_void_p(sw.codes), L.c_void_p(sw.absmax),
                                                     L.c_void_p(flag.data_ptr()), L.c_void_p(st.cuda_stream))
                     L._check("soup_nf4_quantize", st_)
+                elif kind == L.SOUP_WEIGHT_MXFP4:
+                    flag.zero_()
+                    rows, cols = sw.out_features, sw.in_features
+                    ss = L.soup_mx4_scale_stride(cols)
+                    L.soup_mx4_quantize(W, region(sw.codes, n // 2), region(sw.scales, rows * ss), nonfinite=flag)
+                    if flag.item():
+                        raise ValueError(f"layer {l} {name}: non-finite weight")
                 else:
                     region(sw.w, n * 2).view(torch.bfloat16).copy_(W.reshape(-1).to(torch.bfloat16))
             region(v.norm1, cfg.hidden * 2).view(torch.bfloat16).copy_(w["norm1"].reshape(-1))
@@ -439,9 +454,21 @@ class StreamedLoRAModel:
         it = iter(views)
         self.grads = [{"d" + k: next(it) for k in ks} for ks in keys]
         self.master_flat = self.lora_flat.float()
-        self.adam_m = torch.zeros_like(self.grad_flat)
-        self.adam_v = torch.zeros_like(self.grad_flat)
         self.adam_t = 0
+        self.adam_group = None
+        if self.adamw.state_bits == 8:
+            # the flat buffers as one tensor: factors start on multiples of
+            # dp.ALIGN elements, so no block of 32 holds parts of two
+            n = self.grad_flat.numel()
+            self.adam_m, self.adam_v = (torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2))
+            self.adam_m_scale, self.adam_v_scale = (torch.zeros((n + 31) // 32, dtype=torch.uint8, device="cuda")
+                                                    for _ in range(2))
+            self.adam_group = L.AdamWGroup([dict(theta=self.master_flat, theta_bf16=self.lora_flat,
+                                                 grad=self.grad_flat, m=self.adam_m, v=self.adam_v,
+                                                 m_scale=self.adam_m_scale, v_scale=self.adam_v_scale)], state_bits=8)
+        else:
+            self.adam_m = torch.zeros_like(self.grad_flat)
+            self.adam_v = torch.zeros_like(self.grad_flat)
         self.nonfinite = torch.zeros(1, dtype=torch.int32, device="cuda")
         self.lora_s = [L.layer_lora(lo) for lo in self.lora]
         self.grads_s = [L.layer_grads(g) for g in self.grads]
@@ -699,6 +726,10 @@ class StreamedLoRAModel:
         self.nonfinite (device) to 1."""
         o = self.adamw
         self.adam_t += 1
+        if self.adam_group is not None:
+            self.adam_group.step(o.lr, o.beta1, o.beta2, o.eps, o.weight_decay, grad_scale, self.adam_t, seed=o.seed,
+                                 zero_grad=True, nonfinite=self.nonfinite)
+            return
         L.soup_adamw_step(self.master_flat, self.lora_flat, self.grad_flat, self.adam_m, self.adam_v, o.lr,
                           o.beta1, o.beta2, o.eps, o.weight_decay, grad_scale, self.adam_t, zero_grad=True,
                           nonfinite=self.nonfinite)
