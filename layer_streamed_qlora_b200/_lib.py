@@ -315,25 +315,46 @@ def soup_nf4_dequant(codes, absmax, out_f, in_f, W_bf16, stream=None):
                                                       _stream(stream)))
 
 
-def _on_device(fn, dtype=None, **tensors):
-    """Refuses tensors that are not on the current CUDA device, not of `dtype`
-    (when given) or whose last dimension is not contiguous."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
-        if dtype is not None and t.dtype != dtype:
-            raise ValueError(f"{fn}: {name} is {t.dtype}, not {dtype}")
-        if t.numel() > 1 and t.dim() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{fn}: {name}'s last dimension is not contiguous")
+def _refuse(fn, name, t, dev, dtype, n):
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
+    if t.dtype is not dtype:
+        raise ValueError(f"{fn}: {name} is {t.dtype}, not {dtype}")
+    raise ValueError(f"{fn}: {name} must be contiguous with at least {n} elements, not {tuple(t.shape)}")
 
 
-def _whole(fn, n, **tensors):
-    """Refuses tensors that are not contiguous or hold fewer than n elements."""
-    for name, t in tensors.items():
-        if t is not None and (not t.is_contiguous() or t.numel() < n):
-            raise ValueError(f"{fn}: {name} must be contiguous with at least {n} elements, not {tuple(t.shape)}")
+def _ptr(fn, name, t, dev, dtype, n):
+    """Address of a contiguous tensor of `dtype` with at least n elements on device `dev` (None for None)."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or t.numel() < n:
+        _refuse(fn, name, t, dev, dtype, n)
+    return t.data_ptr()
+
+
+def _rows(fn, name, t, dev, dtype, rows, cols):
+    """Address and row stride of a [rows, cols] matrix whose rows may be strided."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or shape[0] != rows:
+        raise ValueError(f"{fn}: {name} must be [{rows}, {cols}], not {tuple(shape)}")
+    stride = t.stride()
+    if t.get_device() != dev or t.dtype is not dtype:
+        _refuse(fn, name, t, dev, dtype, 0)
+    if stride[1] != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"{fn}: the rows of {name} are not contiguous")
+    return t.data_ptr(), stride[0] if rows > 1 else cols
+
+
+def _device_of(fn, name, t):
+    """The current CUDA device, which t has to be on."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
+    return dev
+
+
+def _raw_stream(stream, dev):
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
 
 
 # ---------------------------------------------------------------- MXFP4
@@ -348,28 +369,26 @@ def soup_mx4_quantize(W, codes, scales, W_bf16=None, nonfinite=None, stream=None
     fn = "soup_mx4_quantize"
     if W.dim() != 2 or W.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"{fn}: W must be a float32 or bfloat16 matrix, not {W.dtype} of shape {tuple(W.shape)}")
+    L, dev = lib(), _device_of(fn, "W", W)
     out_f, in_f = W.shape
-    _on_device(fn, W=W)
-    _on_device(fn, torch.uint8, codes=codes, scales=scales)
-    _on_device(fn, torch.bfloat16, W_bf16=W_bf16)
-    _on_device(fn, torch.int32, nonfinite=nonfinite)
-    _whole(fn, out_f * in_f // 2, codes=codes)
-    _whole(fn, out_f * soup_mx4_scale_stride(in_f), scales=scales)
-    _whole(fn, out_f * in_f, W_bf16=W_bf16)
-    _whole(fn, 1, nonfinite=nonfinite)
-    ldw = W.stride(0) if out_f > 1 else in_f
-    _check(fn, lib().soup_mx4_quantize(_p(W), SOUP_TYPE_F32 if W.dtype == torch.float32 else SOUP_TYPE_BF16, out_f,
-                                       in_f, ldw, _p(codes), _p(scales), _p(W_bf16), _p(nonfinite), _stream(stream)))
+    n = out_f * in_f
+    w, ldw = _rows(fn, "W", W, dev, W.dtype, out_f, in_f)
+    _check(fn, L.soup_mx4_quantize(
+        w, SOUP_TYPE_F32 if W.dtype is torch.float32 else SOUP_TYPE_BF16, out_f, in_f, ldw,
+        _ptr(fn, "codes", codes, dev, torch.uint8, n // 2),
+        _ptr(fn, "scales", scales, dev, torch.uint8, out_f * L.soup_mx4_scale_stride(in_f)),
+        _ptr(fn, "W_bf16", W_bf16, dev, torch.bfloat16, n), _ptr(fn, "nonfinite", nonfinite, dev, torch.int32, 1),
+        _raw_stream(stream, dev)))
 
 
 def soup_mx4_dequant(codes, scales, out_f, in_f, W_bf16, stream=None):
     fn = "soup_mx4_dequant"
-    _on_device(fn, torch.uint8, codes=codes, scales=scales)
-    _on_device(fn, torch.bfloat16, W_bf16=W_bf16)
-    _whole(fn, out_f * in_f // 2, codes=codes)
-    _whole(fn, out_f * soup_mx4_scale_stride(in_f), scales=scales)
-    _whole(fn, out_f * in_f, W_bf16=W_bf16)
-    _check(fn, lib().soup_mx4_dequant(_p(codes), _p(scales), out_f, in_f, _p(W_bf16), _stream(stream)))
+    L, dev = lib(), _device_of(fn, "codes", codes)
+    n = out_f * in_f
+    _check(fn, L.soup_mx4_dequant(
+        _ptr(fn, "codes", codes, dev, torch.uint8, n // 2),
+        _ptr(fn, "scales", scales, dev, torch.uint8, out_f * L.soup_mx4_scale_stride(in_f)), out_f, in_f,
+        _ptr(fn, "W_bf16", W_bf16, dev, torch.bfloat16, n), _raw_stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- weights
@@ -390,28 +409,25 @@ def soup_linear_workspace(W: SoupWeight, T) -> int:
     return int(lib().soup_linear_workspace(ctypes.byref(W), int(T)))
 
 
-def _linear(fn, W, a, a_cols, c, c_cols, workspace, stream):
-    for name, t, cols in (("input", a, a_cols), ("output", c, c_cols)):
-        if t.dim() != 2 or t.shape[1] != cols or t.shape[0] != a.shape[0]:
-            raise ValueError(f"{fn}: {name} must be [{a.shape[0]}, {cols}], not {tuple(t.shape)}")
-    _on_device(fn, torch.bfloat16, input=a, output=c)
-    _on_device(fn, workspace=workspace)
-    _whole(fn, 0, workspace=workspace)
-    T = a.shape[0]
-    lda, ldc = (t.stride(0) if T > 1 else cols for t, cols in ((a, a_cols), (c, c_cols)))
-    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(fn, getattr(lib(), fn)(ctypes.byref(W), _p(a), lda, T, _p(c), ldc, _p(workspace) if ws else None, ws,
-                                  _stream(stream)))
+def _linear(fn, f, W, x, x_cols, y, y_cols, workspace, stream):
+    T = x.shape[0] if x.dim() else 0
+    dev = x.get_device()
+    xp, ldx = _rows(fn, "input", x, dev, torch.bfloat16, T, x_cols)
+    yp, ldy = _rows(fn, "output", y, dev, torch.bfloat16, T, y_cols)
+    _device_of(fn, "input", x)
+    ws = 0 if workspace is None else workspace.numel()
+    wp = _ptr(fn, "workspace", workspace, dev, torch.uint8, 0) if ws else None
+    _check(fn, f(ctypes.byref(W), xp, ldx, T, yp, ldy, wp, ws, _raw_stream(stream, dev)))
 
 
 def soup_linear_fwd(W: SoupWeight, x, y, workspace=None, stream=None):
-    """y [T, out] = x [T, in] W^T (bf16; rows may be strided)."""
-    _linear("soup_linear_fwd", W, x, W.in_features, y, W.out_features, workspace, stream)
+    """y [T, out] = x [T, in] W^T (bf16; rows may be strided; workspace: uint8)."""
+    _linear("soup_linear_fwd", lib().soup_linear_fwd, W, x, W.in_features, y, W.out_features, workspace, stream)
 
 
 def soup_linear_bwd(W: SoupWeight, dy, dx, workspace=None, stream=None):
-    """dx [T, in] = dy [T, out] W (bf16; rows may be strided)."""
-    _linear("soup_linear_bwd", W, dy, W.out_features, dx, W.in_features, workspace, stream)
+    """dx [T, in] = dy [T, out] W (bf16; rows may be strided; workspace: uint8)."""
+    _linear("soup_linear_bwd", lib().soup_linear_bwd, W, dy, W.out_features, dx, W.in_features, workspace, stream)
 
 
 # ---------------------------------------------------------------- AdamW group
@@ -428,47 +444,44 @@ class AdamWGroup:
         tensors = [dict(t) for t in tensors]
         if not tensors:
             raise ValueError(f"{fn}: no tensors")
+        dev = _device_of(fn, "theta", tensors[0]["theta"])
         state = torch.uint8 if state_bits == 8 else torch.float32
         grad = tensors[0]["grad"].dtype
         if grad not in (torch.float32, torch.bfloat16):
             raise ValueError(f"{fn}: gradients must be float32 or bfloat16, not {grad}")
+        types = dict(theta=torch.float32, theta_bf16=torch.bfloat16, grad=grad, m=state, v=state)
         arr = (AdamWTensor * len(tensors))()
         for a, t in zip(arr, tensors):
-            n = t["theta"].numel()
-            _on_device(fn, torch.float32, theta=t["theta"])
-            _on_device(fn, torch.bfloat16, theta_bf16=t.get("theta_bf16"))
-            _on_device(fn, grad, grad=t["grad"])
-            _on_device(fn, state, m=t["m"], v=t["v"])
-            sc = {k: t[k] for k in ("m_scale", "v_scale")} if state_bits == 8 else {}
-            _on_device(fn, torch.uint8, **sc)
-            for k in ("theta", "theta_bf16", "grad", "m", "v"):
-                if t.get(k) is not None and (t[k].numel() != n or not t[k].is_contiguous()):
-                    raise ValueError(f"{fn}: {k} must be contiguous with theta's {n} elements")
-            _whole(fn, (n + 31) // 32, **sc)
-            a.n = n
-            if n:
-                for k in ("theta", "theta_bf16", "grad", "m", "v", *sc):
-                    setattr(a, k, t[k].data_ptr() if t.get(k) is not None else None)
+            n = a.n = t["theta"].numel()
+            for k, dtype in types.items():
+                p = _ptr(fn, k, t.get(k), dev, dtype, n)
+                if t.get(k) is not None and t[k].numel() != n:
+                    raise ValueError(f"{fn}: {k} has {t[k].numel()} elements, theta {n}")
+                setattr(a, k, p if n else None)
+            if state_bits == 8:
+                for k in ("m_scale", "v_scale"):
+                    setattr(a, k, _ptr(fn, k, t[k], dev, torch.uint8, (n + 31) // 32) if n else None)
         self._tensors = tensors
         self._handle = AdamWGroupHandle()
         nbytes = lib().soup_adamw_group_bytes(arr, len(tensors))
+        self._dev = dev
         self._tables = torch.empty(max(16, nbytes), dtype=torch.uint8, device="cuda")
         _check(fn, lib().soup_adamw_group_init(arr, len(tensors), int(state_bits),
-                                               SOUP_TYPE_F32 if grad == torch.float32 else SOUP_TYPE_BF16,
+                                               SOUP_TYPE_F32 if grad is torch.float32 else SOUP_TYPE_BF16,
                                                _p(self._tables), self._tables.numel(), ctypes.byref(self._handle),
                                                _stream(stream)))
+        self._ref = ctypes.byref(self._handle)
 
     def step(self, lr, beta1, beta2, eps, weight_decay, grad_scale, t, seed=0, zero_grad=False, nonfinite=None,
              stream=None):
         fn = "soup_adamw_group_step"
-        if self._tables.device.index != torch.cuda.current_device():
-            raise ValueError(f"{fn}: the group is on {self._tables.device}, not on the current CUDA device")
-        if nonfinite is not None:
-            _on_device(fn, torch.int32, nonfinite=nonfinite)
-            _whole(fn, 1, nonfinite=nonfinite)
-        _check(fn, lib().soup_adamw_group_step(ctypes.byref(self._handle), lr, beta1, beta2, eps, weight_decay,
-                                               grad_scale, int(t), int(seed) & 0xFFFFFFFF, 1 if zero_grad else 0,
-                                               _p(nonfinite), _stream(stream)))
+        dev = torch.cuda.current_device()
+        if self._dev != dev:
+            raise ValueError(f"{fn}: the group is on device {self._dev}, not on the current CUDA device")
+        _check(fn, lib().soup_adamw_group_step(self._ref, lr, beta1, beta2, eps, weight_decay, grad_scale, int(t),
+                                               int(seed) & 0xFFFFFFFF, 1 if zero_grad else 0,
+                                               _ptr(fn, "nonfinite", nonfinite, dev, torch.int32, 1),
+                                               _raw_stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- LoRA linear

@@ -32,6 +32,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "ptx.cuh"
 #include "soup_internal.h"
 
 namespace soup {
@@ -49,6 +50,7 @@ struct GroupTensor {
   void* v;
   uint8_t* m_scale;
   uint8_t* v_scale;
+  int64_t v32;  // 1: theta, grad, m and v are 32-byte aligned
 };
 struct GroupChunk {
   uint32_t tensor, chunk;
@@ -64,6 +66,10 @@ struct GroupArgs {
   int32_t* nonfinite;
 };
 
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
 
 // A bijective 32-bit mix (xor-shifts and odd multipliers, Appleby 2011).
@@ -121,80 +127,204 @@ __device__ __forceinline__ float new_v(const GroupArgs& a, float v, float g) {
   return __fadd_rn(__fmul_rn(v, a.beta2), __fmul_rn(__fmul_rn(g, g), a.one_minus_beta2));
 }
 
-template <bool G16>
-__device__ __forceinline__ float load_grad(const void* grad, int64_t i) {
-  if (G16) return __bfloat162float(static_cast<const __nv_bfloat16*>(grad)[i]);
-  return static_cast<const float*>(grad)[i];
+// 8 fp32 values: 32-byte accesses where v32 (p 32-byte aligned), else 16-byte.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8], bool v32) {
+  if (v32) {
+    uint32_t w[8];
+    ptx::ld_global_32B(p, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+  } else {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8], bool v32) {
+  if (v32) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
+    ptx::st_global_32B(p, w);
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
 }
 
+// The largest bits of |x| over a block of 32 (4 lanes of 8), of finite values only.
+__device__ __forceinline__ uint32_t block_top(const float (&x)[8], bool& odd) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  odd = top >= 0x7F800000u;
+  if (odd) {
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (finite(x[i])) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  }
+  top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  return max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+}
+
+// One thread per 8 elements of a chunk: 4 lanes share a block of 32, and all
+// of a tensor's arrays move in 8- to 32-byte accesses.  The elements beyond a
+// tensor's end (in its last chunk alone) count as zeros and are not stored.
 template <int BITS, bool G16>
 __global__ void __launch_bounds__(256) adamw_group_kernel(const GroupArgs a) {
   bool bad = false;
   for (int64_t c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
     const GroupChunk ch = a.chunks[c];
-    const GroupTensor& t = a.tensors[ch.tensor];
-    const int64_t i0 = (int64_t)ch.chunk * CHUNK;
-    const uint32_t key = mix32(mix32(ch.tensor + 0x9E3779B9u * a.t) + a.seed);
-    // element e of a block of 32 is lane e: a warp takes 8 blocks in turn
-    for (int k = 0; k < CHUNK / 256; ++k) {
-      const int64_t i = i0 + k * 256 + threadIdx.x;
-      const bool in_range = i < t.n;
-      float g = 0.f, m = 0.f, v = 0.f, p = 0.f;
-      if (in_range) {
-        const float g_raw = load_grad<G16>(t.grad, i);
-        bad |= !finite(g_raw);
-        g = g_raw * a.grad_scale;
-        p = t.theta[i];
-        if (BITS == 32) {
-          m = static_cast<const float*>(t.m)[i];
-          v = static_cast<const float*>(t.v)[i];
-        } else {
-          m = e4m3_to_f32(static_cast<const uint8_t*>(t.m)[i]) * e8m0(t.m_scale[i >> 5]);
-          v = e5m2_to_f32(static_cast<const uint8_t*>(t.v)[i]) * e8m0(t.v_scale[i >> 5]);
-        }
-      }
-      m = new_m(a, m, g);
-      v = new_v(a, v, g);
-      const float r = __fsqrt_rn(v);
-      if (in_range) {
-        p = __fsub_rn(__fmul_rn(p, a.decay),
-                      __fmul_rn(a.step_size, __fdiv_rn(m, __fadd_rn(__fmul_rn(r, a.inv_sqrt_bc2), a.eps))));
-        t.theta[i] = p;
-        if (t.theta_bf16) reinterpret_cast<__nv_bfloat16*>(t.theta_bf16)[i] = __float2bfloat16_rn(p);
-        if (a.zero_grad) {
-          if (G16) static_cast<uint16_t*>(t.grad)[i] = 0;
-          else static_cast<float*>(t.grad)[i] = 0.f;
-        }
-        if (BITS == 32) {
-          static_cast<float*>(t.m)[i] = m;
-          static_cast<float*>(t.v)[i] = v;
-        }
-      }
-      if (BITS == 8) {
-        uint32_t tm = in_range && finite(m) ? __float_as_uint(m) & 0x7FFFFFFFu : 0u;
-        uint32_t tv = in_range && finite(v) ? __float_as_uint(v) : 0u;
+    const GroupTensor t = a.tensors[ch.tensor];
+    const int64_t i0 = (int64_t)ch.chunk * CHUNK + threadIdx.x * 8;
+    const int64_t left = t.n - i0;
+    const int in = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+    const bool v32 = t.v32;
+    float p[8], g[8], m[8], v[8];
+    if (in == 8) {
+      load8(t.theta + i0, p, v32);
+      if (G16) {
+        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.grad) + i0);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          tm = max(tm, __shfl_xor_sync(0xFFFFFFFFu, tm, o));
-          tv = max(tv, __shfl_xor_sync(0xFFFFFFFFu, tv, o));
+        for (int i = 0; i < 4; ++i) {
+          g[2 * i] = __uint_as_float(ws[i] << 16);
+          g[2 * i + 1] = __uint_as_float(ws[i] & 0xFFFF0000u);
         }
-        float um, uv;
-        const uint32_t sm = block_scale<E4M3>(tm, um), sv = block_scale<E5M2>(tv, uv);
-        if (in_range) {
-          const uint32_t h = mix32((uint32_t)(i >> 1) + key);
-          const uint32_t rnd = (i & 1) ? h >> 16 : h & 0xFFFFu;
-          uint32_t cm = encode_stochastic<E4M3>(fabsf(m) * um, rnd) | (__float_as_uint(m) >> 31 << 7);
-          if (!finite(m)) cm = 0x7F;
-          uint32_t cv = encode_stochastic<E5M2>(v * uv, rnd);
-          if (cv == 0 && v > 0.f) cv = 1;
-          if (!finite(v)) cv = 0x7F;
-          static_cast<uint8_t*>(t.m)[i] = (uint8_t)cm;
-          static_cast<uint8_t*>(t.v)[i] = (uint8_t)cv;
-          if ((i & 31) == 0) {
-            t.m_scale[i >> 5] = (uint8_t)sm;
-            t.v_scale[i >> 5] = (uint8_t)sv;
-          }
+      } else {
+        load8(static_cast<const float*>(t.grad) + i0, g, v32);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool ok = i < in;
+        p[i] = ok ? t.theta[i0 + i] : 0.f;
+        if (G16) g[i] = ok ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.grad)[i0 + i]) : 0.f;
+        else g[i] = ok ? static_cast<const float*>(t.grad)[i0 + i] : 0.f;
+      }
+    }
+    if (BITS == 32) {
+      const float *ms = static_cast<const float*>(t.m) + i0, *vs = static_cast<const float*>(t.v) + i0;
+      if (in == 8) {
+        load8(ms, m, v32);
+        load8(vs, v, v32);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          m[i] = i < in ? ms[i] : 0.f;
+          v[i] = i < in ? vs[i] : 0.f;
         }
+      }
+    } else {
+      const uint8_t *ms = static_cast<const uint8_t*>(t.m) + i0, *vs = static_cast<const uint8_t*>(t.v) + i0;
+      uint32_t mw[2] = {0, 0}, vw[2] = {0, 0};
+      float sm = 0.f, sv = 0.f;
+      if (in == 8) {
+        const uint2 x = *reinterpret_cast<const uint2*>(ms), y = *reinterpret_cast<const uint2*>(vs);
+        mw[0] = x.x; mw[1] = x.y; vw[0] = y.x; vw[1] = y.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i >= in) break;
+          mw[i >> 2] |= (uint32_t)ms[i] << (8 * (i & 3));
+          vw[i >> 2] |= (uint32_t)vs[i] << (8 * (i & 3));
+        }
+      }
+      if (in > 0) {
+        sm = e8m0(t.m_scale[i0 >> 5]);
+        sv = e8m0(t.v_scale[i0 >> 5]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m[i] = e4m3_to_f32((mw[i >> 2] >> (8 * (i & 3))) & 0xFFu) * sm;
+        v[i] = e5m2_to_f32((vw[i >> 2] >> (8 * (i & 3))) & 0xFFu) * sv;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      bad |= !finite(g[i]);
+      const float gi = g[i] * a.grad_scale;
+      m[i] = new_m(a, m[i], gi);
+      v[i] = new_v(a, v[i], gi);
+      p[i] = __fsub_rn(__fmul_rn(p[i], a.decay),
+                       __fmul_rn(a.step_size,
+                                 __fdiv_rn(m[i], __fadd_rn(__fmul_rn(__fsqrt_rn(v[i]), a.inv_sqrt_bc2), a.eps))));
+    }
+    if (in == 8) {
+      store8(t.theta + i0, p, v32);
+      if (t.theta_bf16) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+        *reinterpret_cast<uint4*>(t.theta_bf16 + i0) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (a.zero_grad) {
+        if (G16) {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(t.grad) + i0) = make_uint4(0, 0, 0, 0);
+        } else {
+          const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          store8(static_cast<float*>(t.grad) + i0, z, v32);
+        }
+      }
+      if (BITS == 32) {
+        store8(static_cast<float*>(t.m) + i0, m, v32);
+        store8(static_cast<float*>(t.v) + i0, v, v32);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i >= in) break;
+        t.theta[i0 + i] = p[i];
+        if (t.theta_bf16) t.theta_bf16[i0 + i] = (uint16_t)(pack_bf16x2(p[i], 0.f) & 0xFFFFu);
+        if (a.zero_grad) {
+          if (G16) static_cast<uint16_t*>(t.grad)[i0 + i] = 0;
+          else static_cast<float*>(t.grad)[i0 + i] = 0.f;
+        }
+        if (BITS == 32) {
+          static_cast<float*>(t.m)[i0 + i] = m[i];
+          static_cast<float*>(t.v)[i0 + i] = v[i];
+        }
+      }
+    }
+    if (BITS == 8) {
+      const uint32_t key = mix32(mix32(ch.tensor + 0x9E3779B9u * a.t) + a.seed);
+      bool odd_m, odd_v;
+      float um, uv;
+      const uint32_t sm = block_scale<E4M3>(block_top(m, odd_m), um);
+      const uint32_t sv = block_scale<E5M2>(block_top(v, odd_v), uv);
+      uint32_t mw[2] = {0, 0}, vw[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const uint32_t h = mix32((uint32_t)((i0 + i) >> 1) + key);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int j = i + k;
+          const uint32_t rnd = k ? h >> 16 : h & 0xFFFFu;
+          uint32_t cm = encode_stochastic<E4M3>(fabsf(m[j]) * um, rnd) | (__float_as_uint(m[j]) >> 31 << 7);
+          uint32_t cv = encode_stochastic<E5M2>(v[j] * uv, rnd);
+          if (cv == 0 && v[j] > 0.f) cv = 1;
+          if (odd_m && !finite(m[j])) cm = 0x7F;
+          if (odd_v && !finite(v[j])) cv = 0x7F;
+          mw[j >> 2] |= cm << (8 * (j & 3));
+          vw[j >> 2] |= cv << (8 * (j & 3));
+        }
+      }
+      uint8_t *ms = static_cast<uint8_t*>(t.m) + i0, *vs = static_cast<uint8_t*>(t.v) + i0;
+      if (in == 8) {
+        *reinterpret_cast<uint2*>(ms) = make_uint2(mw[0], mw[1]);
+        *reinterpret_cast<uint2*>(vs) = make_uint2(vw[0], vw[1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i >= in) break;
+          ms[i] = (uint8_t)(mw[i >> 2] >> (8 * (i & 3)));
+          vs[i] = (uint8_t)(vw[i >> 2] >> (8 * (i & 3)));
+        }
+      }
+      if ((threadIdx.x & 3) == 0 && in > 0) {
+        t.m_scale[i0 >> 5] = (uint8_t)sm;
+        t.v_scale[i0 >> 5] = (uint8_t)sv;
       }
     }
   }
@@ -246,7 +376,9 @@ extern "C" soup_status soup_adamw_group_init(const soup_adamw_tensor* tensors, i
       SOUP_CHECK(soup_aligned(s.theta, 16) && soup_aligned(s.theta_bf16, 16) && soup_aligned(s.grad, 16) &&
                      soup_aligned(s.m, 16) && soup_aligned(s.v, 16),
                  SOUP_ERR_ALIGN, "%s: tensor %d: theta, theta_bf16, grad, m and v must be 16-byte aligned", fn, i);
-      gt[i] = GroupTensor{s.n, s.theta, s.theta_bf16, s.grad, s.m, s.v, s.m_scale, s.v_scale};
+      const int64_t v32 = soup_aligned(s.theta, 32) && soup_aligned(s.grad, 32) && soup_aligned(s.m, 32) &&
+                          soup_aligned(s.v, 32);
+      gt[i] = GroupTensor{s.n, s.theta, s.theta_bf16, s.grad, s.m, s.v, s.m_scale, s.v_scale, v32};
       for (int64_t c = 0; c < chunks_of(s.n); ++c) gc.push_back(GroupChunk{(uint32_t)i, (uint32_t)c});
       total += s.n;
       const size_t gs = grad_type == SOUP_TYPE_F32 ? 4 : 2, ss = state_bits / 8;
