@@ -354,7 +354,7 @@ def _device_of(fn, name, t):
 
 
 def _raw_stream(stream, dev):
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 # ---------------------------------------------------------------- MXFP4

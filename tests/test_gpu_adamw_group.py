@@ -86,7 +86,7 @@ def test_32_bit_states(grad, zero):
         assert (np.abs(now["m"] - m) <= 6 * 2.0 ** -24 * sm).all()
         assert (np.abs(now["v"] - v) <= 6 * 2.0 ** -24 * v + 1e-45).all()
         # theta: decay and subtraction (and the decay's constant); the update: m's error over the denominator
-        # and about eight roundings of its own
+        # and sixteen fp32 half steps for its quotient, root, sum, products and the constants' roundings
         derr = hp["lr"] / (1 - hp["beta1"] ** 9) * 6 * 2.0 ** -24 * sm / (np.sqrt(v / (1 - hp["beta2"] ** 9)) + hp["eps"])
         assert (np.abs(now["theta"] - th) <= 4 * 2.0 ** -24 * np.abs(t0["theta"]) + 16 * 2.0 ** -24 * np.abs(up) + derr).all()
         if "theta_bf16" in now:
@@ -97,7 +97,9 @@ def test_32_bit_states(grad, zero):
 @pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("zero", [False, True])
 def test_8_bit_states_code_for_code(grad, zero):
-    """Every operation up to the codes is one correctly rounded fp32 operation, so the codes are equal."""
+    """Every operation up to the codes is one correctly rounded fp32 operation, so the codes are equal.  theta
+    is not: its update's quotient, root, sum and products are off by up to eight fp32 steps of 2^-23 (2^-20), the
+    decayed parameter by one rounding, the difference by another of a result below their sum."""
     rng = np.random.default_rng(1)
     ts = [make(n, 8, grad, rng, bf16=i % 3 != 1) for i, n in enumerate(SIZES)]
     before = [snapshot(t) for t in ts]
@@ -107,9 +109,10 @@ def test_8_bit_states_code_for_code(grad, zero):
         n = t0["theta"].size
         p, m, v = moments32(t0, 70_001, HP)
         now = snapshot(t)
-        np.testing.assert_array_equal(now["theta"], p)
+        up = np.abs(p - t0["theta"] * np.float32(1.0 - HP["lr"] * HP["weight_decay"]))
+        assert (np.abs(now["theta"].astype(np.float64) - p) <= 2.0 ** -20 * up + 2.0 ** -22 * np.abs(t0["theta"])).all()
         if "theta_bf16" in now:
-            np.testing.assert_array_equal(now["theta_bf16"], round_to_bf16(p))
+            np.testing.assert_array_equal(now["theta_bf16"], round_to_bf16(now["theta"]))
         rnd = mx.random16(n, k, 99, 70_001)
         for name, x in (("m", m), ("v", v)):
             c, s = mx.state_encode_stochastic(x.astype(np.float64), rnd, TABLE[name], keep_nonzero=name == "v")
