@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "gemm.h"
+#include "linear.h"
 #include "lora_internal.h"
 
 namespace soup {
@@ -57,6 +58,8 @@ extern "C" soup_status soup_linear_fwd(const soup_weight* W, const uint16_t* x, 
   SOUP_TRY(check_linear("soup_linear_fwd", W, x, ldx, W ? W->in_features : 0, T, y, ldy, W ? W->out_features : 0,
                         workspace, workspace_bytes));
   if (T == 0) return SOUP_OK;
+  if (W->kind == SOUP_WEIGHT_MXFP4 && T <= MX4_FEW_TOKENS)
+    return mx4_few(W, x, ldx, (int)T, y, ldy, static_cast<cudaStream_t>(stream));
   GemmDesc g;
   g.M = (int)T; g.N = (int)W->out_features; g.K = (int)W->in_features;
   g.A = Mat{x, T, W->in_features, ldx};

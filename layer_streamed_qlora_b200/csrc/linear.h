@@ -1,0 +1,13 @@
+// Kernels of the frozen projection beside the GEMM engine.
+#pragma once
+
+#include "soup_internal.h"
+
+namespace soup {
+
+// y [T, out] = x [T, in] W^T, W MXFP4, 1 <= T <= MX4_FEW_TOKENS.
+constexpr int MX4_FEW_TOKENS = 32;
+soup_status mx4_few(const soup_weight* W, const uint16_t* x, int64_t ldx, int T, uint16_t* y, int64_t ldy,
+                    cudaStream_t st);
+
+}  // namespace soup

@@ -1,0 +1,156 @@
+// y = x W^T over an MXFP4 W for few tokens.
+//
+// With T tokens a weight of 4.25 bits does 2 T flops: up to a few dozen tokens
+// the product is bound by reading W once, and the 256-wide tiles of the GEMM
+// engine leave most SMs without work.  Here W is the M side of
+// mma.sync.m16n8k16 (16 weight rows by 8 tokens): a CTA owns 16 * MT rows and
+// all of K, its 8 warps take K in turns of 128, every thread loads one 16-byte
+// block of 32 codes per row and turn straight into registers, and the 8
+// partial sums meet in shared memory in warp order.  No tile of W passes
+// through shared memory, nothing is split across CTAs, and the order of the
+// sums does not depend on the launch.
+//
+// The order of k inside a turn is free as long as both operands agree, so a
+// thread's four k of one instruction are those that its codes decode to
+// without permutes: of 8 neighbouring codes the pairs (0, 4), (1, 5) and then
+// (2, 6), (3, 7).  x is permuted to match when it is loaded.
+#include <algorithm>
+
+#include "linear.h"
+#include "mx4.cuh"
+
+namespace soup {
+namespace {
+
+constexpr int WARPS = 8;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The 8 codes of a word as 4 bf16x2 pairs (k, k + 4) times the scale.
+__device__ __forceinline__ void decode_pairs(uint32_t w, uint32_t scale2, uint32_t (&p)[4]) {
+  constexpr uint32_t MAG = 0x01C001C0u, SGN = 0x80008000u, UP = 0x7E807E80u;  // as in mx4_decode8
+  p[0] = mul_bf16x2(mul_bf16x2(((w << 6) & MAG) | ((w << 12) & SGN), UP), scale2);
+  p[1] = mul_bf16x2(mul_bf16x2(((w << 2) & MAG) | ((w << 8) & SGN), UP), scale2);
+  p[2] = mul_bf16x2(mul_bf16x2(((w >> 2) & MAG) | ((w << 4) & SGN), UP), scale2);
+  p[3] = mul_bf16x2(mul_bf16x2(((w >> 6) & MAG) | (w & SGN), UP), scale2);
+}
+
+// MT: 16-row groups of W per CTA; NT: groups of 8 tokens; DEPTH: turns whose
+// loads of W are in flight together.
+template <int MT, int NT, int DEPTH>
+__global__ void __launch_bounds__(32 * WARPS) mx4_few_kernel(const uint8_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales, int N, int K,
+                                                            int64_t scale_stride, const uint16_t* __restrict__ x,
+                                                            int64_t ldx, int T, uint16_t* __restrict__ y, int64_t ldy) {
+  __shared__ float part[WARPS][NT * 8][16 * MT + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  const int row0 = blockIdx.x * 16 * MT, blocks = K / 32, turns = (blocks + 3) / 4;
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.f;
+
+  for (int turn0 = warp; turn0 < turns; turn0 += WARPS * DEPTH) {
+    uint4 w[DEPTH][2 * MT];
+    uint32_t s[DEPTH][2 * MT];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      const int b = (turn0 + d * WARPS) * 4 + tq;
+#pragma unroll
+      for (int r = 0; r < 2 * MT; ++r) {
+        const int row = row0 + 8 * r + g;
+        const bool ok = b < blocks && row < N;
+        w[d][r] = ok ? __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)row * (K / 2)) + b) : make_uint4(0, 0, 0, 0);
+        s[d][r] = ok ? __ldg(scales + row * scale_stride + b) : 0u;
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      const int b = (turn0 + d * WARPS) * 4 + tq;
+      if (turn0 + d * WARPS >= turns) break;
+      uint32_t sc[2 * MT];
+#pragma unroll
+      for (int r = 0; r < 2 * MT; ++r) sc[r] = mx4_scale_bf16x2(s[d][r]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t bx[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int t = 8 * j + g;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (t < T && b < blocks) v = __ldg(reinterpret_cast<const uint4*>(x + t * ldx + (int64_t)b * 32) + u);
+          bx[j][0] = __byte_perm(v.x, v.z, 0x5410);
+          bx[j][1] = __byte_perm(v.x, v.z, 0x7632);
+          bx[j][2] = __byte_perm(v.y, v.w, 0x5410);
+          bx[j][3] = __byte_perm(v.y, v.w, 0x7632);
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const uint4 lo = w[d][2 * i], hi = w[d][2 * i + 1];
+          uint32_t p[4], q[4];
+          decode_pairs(u == 0 ? lo.x : u == 1 ? lo.y : u == 2 ? lo.z : lo.w, sc[2 * i], p);
+          decode_pairs(u == 0 ? hi.x : u == 1 ? hi.y : u == 2 ? hi.z : hi.w, sc[2 * i + 1], q);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma16816(acc[i][j], p[0], q[0], p[1], q[1], bx[j][0], bx[j][1]);
+            mma16816(acc[i][j], p[2], q[2], p[3], q[3], bx[j][2], bx[j][3]);
+          }
+        }
+      }
+    }
+  }
+  // acc[i][j]: rows 16 i + g (+ 8), tokens 8 j + 2 tq (+ 1)
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) part[warp][8 * j + 2 * tq + (k & 1)][16 * i + g + 8 * (k >> 1)] = acc[i][j][k];
+  __syncthreads();
+  for (int e = threadIdx.x; e < 16 * MT * NT * 8; e += 32 * WARPS) {
+    const int r = e % (16 * MT), t = e / (16 * MT);
+    if (t >= T || row0 + r >= N) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) v += part[k][t][r];
+    const __nv_bfloat16 o = __float2bfloat16_rn(v);
+    y[t * ldy + row0 + r] = *reinterpret_cast<const uint16_t*>(&o);
+  }
+}
+
+template <int MT, int NT, int DEPTH>
+soup_status launch_few(const soup_weight* W, const uint16_t* x, int64_t ldx, int T, uint16_t* y, int64_t ldy,
+                       cudaStream_t st) {
+  const int N = (int)W->out_features, K = (int)W->in_features;
+  mx4_few_kernel<MT, NT, DEPTH><<<(N + 16 * MT - 1) / (16 * MT), 32 * WARPS, 0, st>>>(
+      W->codes, W->scales, N, K, mx4_scale_stride(K), x, ldx, T, y, ldy);
+  SOUP_LAUNCH_CHECK();
+  return SOUP_OK;
+}
+
+}  // namespace
+
+soup_status mx4_few(const soup_weight* W, const uint16_t* x, int64_t ldx, int T, uint16_t* y, int64_t ldy,
+                    cudaStream_t st) {
+  const double n = (double)W->out_features * W->in_features;
+  profile_begin(st, GC_NF4_FWD, 2.0 * T * n, n * (0.5 + 1.0 / 32) + 2.0 * T * (W->out_features + W->in_features));
+  soup_status r;
+  if (T <= 8) r = launch_few<1, 1, 4>(W, x, ldx, T, y, ldy, st);
+  else if (T <= 16) r = launch_few<1, 2, 2>(W, x, ldx, T, y, ldy, st);
+  else r = launch_few<2, 4, 2>(W, x, ldx, T, y, ldy, st);
+  SOUP_TRY(r);
+  profile_end(st);
+  return SOUP_OK;
+}
+
+}  // namespace soup
