@@ -253,17 +253,23 @@ __device__ __forceinline__ uint4 decode8_pairs(uint32_t w, const uint8_t* lut_by
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// 8 MXFP4 codes times their block's scale (2^(s - 127) as bf16x2).
-__device__ __forceinline__ uint4 decode8_mx4(uint32_t w, uint32_t scale2) {
-  uint32_t o[4];
-  mx4_decode8(w, scale2, o);
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 __device__ __forceinline__ void st_shared_v4(void* p, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(ptx::smem_u32(p)), "r"(v.x),
                "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
+}
+
+// One MXFP4 block of 32 (zeros where !valid) into units unit0..unit0+3 of a
+// swizzled 128-byte row: unit u is stored at u ^ swz.
+__device__ __forceinline__ void decode_block_mx4(const uint32_t (&codes)[4], uint32_t scale, bool valid, uint8_t* row,
+                                                 int unit0, int swz) {
+  uint32_t w[4], v[16];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) w[u] = valid ? codes[u] : 0u;
+  mx4_decode_block(w, valid ? scale : 0u, v);
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    st_shared_v4(row + (((unit0 + u) ^ swz) << 4), make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
 }
 
 template <int NWORDS>
@@ -957,7 +963,7 @@ __global__ void __launch_bounds__(32 * (2 + (b_coded(BMD) ? 8 : 4)), 1)
           uint32_t w[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) w[u] = wn[u];
-          const uint32_t scale2 = mx4_scale_bf16x2(scn);
+          const uint32_t scale = scn;
           const bool valid = nvalid && it * BK + h * 32 < args.K;
           if (nvalid && (it + 1) * BK + h * 32 < args.K) {
             load_codes(src + (size_t)(it + 1) * 32, wn);
@@ -969,12 +975,7 @@ __global__ void __launch_bounds__(32 * (2 + (b_coded(BMD) ? 8 : 4)), 1)
             break;
           }
           if (it < num_kb) {
-            uint8_t* b = sB + s * C::B_STAGE;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint4 v = valid ? decode8_mx4(w[u], scale2) : make_uint4(0, 0, 0, 0);
-              st_shared_v4(b + row * 128 + (((h * 4 + u) ^ (row & 7)) << 4), v);
-            }
+            decode_block_mx4(w, scale, valid, sB + s * C::B_STAGE + row * 128, h * 4, row & 7);
             ptx::fence_proxy_async_smem();
           }
           __syncwarp();
@@ -1193,9 +1194,10 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* sk_last = reinterpret_cast<volatile int*>(tmem_slot + 2);
 
-  const int warp = threadIdx.x >> 5;
+  // warp-uniform, and known to the compiler as such
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = ptx::cluster_ctarank();
+  const uint32_t rank = __shfl_sync(0xFFFFFFFFu, ptx::cluster_ctarank(), 0);
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int num_kb = args.num_kb;
   const bool paired = args.pair_off > 0;
@@ -1241,57 +1243,58 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
   ptx::tc_fence_before();
   ptx::cluster_sync();
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
 
+  // The TMA and MMA warps run their loops as a whole, and one lane issues: in
+  // a loop of a single lane every operand would pass from vector to uniform
+  // registers, and the issuing thread, not the tensor core, set the pace.
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
-      int gi = 0;
-      bool ok = true;
-      for (int j = 0; j < nitems && ok; ++j) {
-        const PairItem wi = pair_item(args, j, pair, npairs);
-        const PairTile tl = pair_tile(args, wi.t, mtiles, rank);
-        const int r0 = paired ? (rank == 0 ? tl.nb : args.pair_off + tl.nb) : tl.n0 + (int)rank * 128;
-        const int c0 = tl.n0 + (int)rank * 128;
-        const int it_end = item_end(wi);
-        for (int it = wi.kb0; it < it_end; ++it, ++gi) {
-          const int s = gi % STAGES;
-          const uint32_t ph = (gi / STAGES) & 1;
-          if (!ptx::mbar_wait_bounded(&empty[s], ph ^ 1, abort_flag)) {
-            atomicOr(args.err, 1);
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          uint8_t* a = sA + s * C::A_STAGE;
-          uint8_t* b = sB + s * C::B_STAGE;
-          const bool tail = it >= num_kb;
-          const uint32_t bytes = tail ? (uint32_t)(A_STAGE_BYTES + C::B_STAGE)
-                                      : (uint32_t)(C::A_STAGE + (NF4 ? 0 : C::B_STAGE));
+    const bool leader = ptx::elect_one();
+    const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
+    // innermost coordinate of the absmax / scale box: 4 absmax of 64 elements,
+    // or 16 scales of 32, from a multiple of 16 bytes
+    auto sbox = [](int e) { return MX4 ? (e / 32) & ~15 : (e / 64) & ~3; };
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int j = 0; j < nitems && ok; ++j) {
+      const PairItem wi = pair_item(args, j, pair, npairs);
+      const PairTile tl = pair_tile(args, wi.t, mtiles, rank);
+      const int r0 = paired ? (rank == 0 ? tl.nb : args.pair_off + tl.nb) : tl.n0 + (int)rank * 128;
+      const int c0 = tl.n0 + (int)rank * 128;
+      const int it_end = item_end(wi);
+      for (int it = wi.kb0; it < it_end; ++it) {
+        if (!ptx::mbar_wait_warp(&empty[s], ph ^ 1, abort_flag)) {
+          atomicOr(args.err, 1);
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        uint8_t* a = sA + s * C::A_STAGE;
+        uint8_t* b = sB + s * C::B_STAGE;
+        const bool tail = it >= num_kb;
+        const uint32_t bytes =
+            tail ? (uint32_t)(A_STAGE_BYTES + C::B_STAGE) : (uint32_t)(C::A_STAGE + (NF4 ? 0 : C::B_STAGE));
+        const uint32_t bar = full0 + s * 8;
+        if (leader && !tail) {
           if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * bytes);
-          const uint32_t bar = full0 + s * 8;
-          if (!tail) {
-            ptx::tma_load_2d_pair(a, &tmA, bar, it * BK, tl.m0);
-            if (DUAL) ptx::tma_load_2d_pair(a + A_STAGE_BYTES, &tmA3, bar, it * BK, tl.m0);
-            if constexpr (!NF4) {
-              // bf16 B: this CTA's 128 rows (K-major; paired tiles: its half
-              // of the pair) or 128 columns as two 64-wide chunks (MN-major)
-              if constexpr (!B_MN) {
-                ptx::tma_load_2d_pair(b, &tmB, bar, it * BK, r0);
-              } else {
-                ptx::tma_load_2d_pair(b, &tmB, bar, c0, it * BK);
-                ptx::tma_load_2d_pair(b + 8192, &tmB, bar, c0 + 64, it * BK);
-              }
-              continue;
+          ptx::tma_load_2d_pair(a, &tmA, bar, it * BK, tl.m0);
+          if (DUAL) ptx::tma_load_2d_pair(a + A_STAGE_BYTES, &tmA3, bar, it * BK, tl.m0);
+          if constexpr (!NF4) {
+            // bf16 B: this CTA's 128 rows (K-major; paired tiles: its half of
+            // the pair) or 128 columns as two 64-wide chunks (MN-major)
+            if constexpr (!B_MN) {
+              ptx::tma_load_2d_pair(b, &tmB, bar, it * BK, r0);
+            } else {
+              ptx::tma_load_2d_pair(b, &tmB, bar, c0, it * BK);
+              ptx::tma_load_2d_pair(b + 8192, &tmB, bar, c0 + 64, it * BK);
             }
+          } else {
             uint8_t* c = sC + s * C::C_STAGE;
             uint8_t* sc = sS + s * C::S_STAGE;
             const int ip = it + 12;
             ptx::mbar_arrive_expect_tx(&cfull[s], (uint32_t)(C::C_STAGE + (B_MN ? 1024 : 2048)));
-            // innermost coordinate of the absmax / scale box: 4 absmax of 64
-            // elements, or 16 scales of 32, from a multiple of 16 bytes
-            auto sbox = [](int e) { return MX4 ? (e / 32) & ~15 : (e / 64) & ~3; };
             if (!B_MN) {
               ptx::tma_load_2d(c, &tmB, &cfull[s], it * 32, r0);
               ptx::tma_load_2d(sc, &tmA2, &cfull[s], sbox(it * BK), r0);
@@ -1307,80 +1310,90 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
                 ptx::tma_prefetch_l2_2d(&tmA2, sbox(c0), ip * BK);
               }
             }
-          } else {
-            if (NF4) ptx::mbar_arrive(&cfull[s]);  // keeps cfull's phase in step with the slot's uses
-            ptx::tma_load_2d_pair(a, &tmTA, bar, tl.m0, tl.tail_row);
-            ptx::tma_load_2d_pair(a + 8192, &tmTA, bar, tl.m0 + 64, tl.tail_row);
-            if (!B_MN) {
-              if (paired) {
-                ptx::tma_load_2d_pair(b, &tmTB, bar, 0, tl.nb + (int)rank * 64);
-                ptx::tma_load_2d_pair(b + 8192, &tmTB, bar, 0, args.pair_off + tl.nb + (int)rank * 64);
-              } else {
-                ptx::tma_load_2d_pair(b, &tmTB, bar, 0, tl.n0 + (int)rank * 128);
-              }
+          }
+        } else if (leader) {
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * bytes);
+          if (NF4) ptx::mbar_arrive(&cfull[s]);  // keeps cfull's phase in step with the slot's uses
+          ptx::tma_load_2d_pair(a, &tmTA, bar, tl.m0, tl.tail_row);
+          ptx::tma_load_2d_pair(a + 8192, &tmTA, bar, tl.m0 + 64, tl.tail_row);
+          if (!B_MN) {
+            if (paired) {
+              ptx::tma_load_2d_pair(b, &tmTB, bar, 0, tl.nb + (int)rank * 64);
+              ptx::tma_load_2d_pair(b + 8192, &tmTB, bar, 0, args.pair_off + tl.nb + (int)rank * 64);
             } else {
-              ptx::tma_load_2d_pair(b, &tmTB, bar, c0, 0);
-              ptx::tma_load_2d_pair(b + 8192, &tmTB, bar, c0 + 64, 0);
+              ptx::tma_load_2d_pair(b, &tmTB, bar, 0, tl.n0 + (int)rank * 128);
             }
+          } else {
+            ptx::tma_load_2d_pair(b, &tmTB, bar, c0, 0);
+            ptx::tma_load_2d_pair(b + 8192, &tmTB, bar, c0 + 64, 0);
           }
         }
+        if (++s == STAGES) { s = 0; ph ^= 1; }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------- MMA issuer (even CTA of the pair)
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc_main = ptx::idesc_bf16(2 * BM, BN, 0, B_MN ? 1 : 0);
       constexpr uint32_t idesc_tail = ptx::idesc_bf16(2 * BM, BN, 1, B_MN ? 1 : 0);
       constexpr uint32_t idesc_half = ptx::idesc_bf16(2 * BM, BN / 2, 1, B_MN ? 1 : 0);
-      int gi = 0, lt = 0;
+      constexpr uint32_t HI = ptx::desc_hi_sw128(1024);
+      constexpr uint32_t BK_STEP = B_MN ? KSTEP_MN >> 4 : 2;  // descriptor units of 16 bytes
+      const bool leader = ptx::elect_one();
+      const uint32_t a0 = ptx::desc_lo(ptx::smem_u32(sA), 16), at0 = ptx::desc_lo(ptx::smem_u32(sA), CHUNK_BYTES);
+      const uint32_t b0 = ptx::desc_lo(ptx::smem_u32(sB), B_MN ? CHUNK_BYTES : 16);
+      int s = 0, lt = 0;
+      uint32_t ph = 0;
       bool ok = true;
       for (int j = 0; j < nitems && ok; ++j, ++lt) {
         const PairItem wi = pair_item(args, j, pair, npairs);
         const int it_end = item_end(wi);
         const int ab = lt & 1;
-        if (!ptx::mbar_wait_bounded(&acc_empty[ab], ((lt >> 1) & 1) ^ 1, abort_flag)) {
+        if (!ptx::mbar_wait_warp(&acc_empty[ab], ((lt >> 1) & 1) ^ 1, abort_flag)) {
           atomicOr(args.err, 1);
           *abort_flag = 1;
           break;
         }
         ptx::tc_fence_after();
         const uint32_t tacc = tmem + (uint32_t)(ab * BN);
-        for (int it = wi.kb0; it < it_end; ++it, ++gi) {
-          const int s = gi % STAGES;
-          const uint32_t ph = (gi / STAGES) & 1;
-          if (!ptx::mbar_wait_bounded(&full[s], ph, abort_flag)) {
+        for (int it = wi.kb0; it < it_end; ++it) {
+          if (!ptx::mbar_wait_warp(&full[s], ph, abort_flag)) {
             atomicOr(args.err, 1);
             *abort_flag = 1;
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t a_base = ptx::smem_u32(sA + s * C::A_STAGE);
-          const uint32_t b_base = ptx::smem_u32(sB + s * C::B_STAGE);
-          const bool tail = it >= num_kb;
-          if (tail && paired) {
+          const uint32_t alo = a0 + s * (C::A_STAGE >> 4), blo = b0 + s * (C::B_STAGE >> 4);
+          if (leader) {
+            if (it < num_kb) {
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint64_t ad = ptx::smem_desc_sw128(a_base + hf * 2048, 8192, 1024);
-              const uint64_t bd = ptx::smem_desc_sw128(b_base + hf * 8192, 16, 1024);
-              ptx::mma_bf16_pair(tacc + hf * (BN / 2), ad, bd, idesc_half, 1u);
+              for (int k = 0; k < 4; ++k) {
+                const uint64_t bd = ptx::desc_of(blo + k * BK_STEP, HI);
+                ptx::mma_bf16_pair(tacc, ptx::desc_of(alo + k * 2, HI), bd, idesc_main,
+                                   (it > wi.kb0 || k > 0) ? 1u : 0u);
+                if (DUAL)
+                  ptx::mma_bf16_pair(tacc, ptx::desc_of(alo + (A_STAGE_BYTES >> 4) + k * 2, HI), bd, idesc_main, 1u);
+              }
+            } else {
+              // LoRA tail: MN-major A of up to 64 rows of u
+              const uint32_t tlo = at0 + s * (C::A_STAGE >> 4);
+              if (paired) {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                  ptx::mma_bf16_pair(tacc + hf * (BN / 2), ptx::desc_of(tlo + hf * (2048 >> 4), HI),
+                                     ptx::desc_of(blo + hf * (8192 >> 4), HI), idesc_half, 1u);
+              } else {
+                for (int k = 0; k < args.tail_ksteps; ++k)
+                  ptx::mma_bf16_pair(tacc, ptx::desc_of(tlo + k * (KSTEP_MN >> 4), HI),
+                                     ptx::desc_of(blo + k * BK_STEP, HI), idesc_tail, 1u);
+              }
             }
-          } else {
-            const int nk = tail ? args.tail_ksteps : 4;
-            for (int k = 0; k < nk; ++k) {
-              const uint64_t ad = tail ? ptx::smem_desc_sw128(a_base + k * KSTEP_MN, CHUNK_BYTES, 1024)
-                                       : ptx::smem_desc_sw128(a_base + k * 32, 16, 1024);
-              const uint64_t bd = B_MN ? ptx::smem_desc_sw128(b_base + k * KSTEP_MN, CHUNK_BYTES, 1024)
-                                       : ptx::smem_desc_sw128(b_base + k * 32, 16, 1024);
-              ptx::mma_bf16_pair(tacc, ad, bd, tail ? idesc_tail : idesc_main, (it > wi.kb0 || k > 0) ? 1u : 0u);
-              if (DUAL && !tail)
-                ptx::mma_bf16_pair(tacc, ptx::smem_desc_sw128(a_base + A_STAGE_BYTES + k * 32, 16, 1024), bd,
-                                   idesc_main, 1u);
-            }
+            ptx::mma_commit_pair(&empty[s], 3);
           }
-          ptx::mma_commit_pair(&empty[s], 3);
+          if (++s == STAGES) { s = 0; ph ^= 1; }
         }
-        if (ok) ptx::mma_commit_pair(&acc_full[ab], 3);
+        if (ok && leader) ptx::mma_commit_pair(&acc_full[ab], 3);
       }
     }
   } else if (warp < 10) {
@@ -1438,13 +1451,9 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
           if constexpr (MX4) {
             // one block of 32 per thread; K-major: the blocks of a last
             // k-block that K ends inside are zeros (their scale bytes are padding)
-            const uint32_t scale2 = mx4_scale_bf16x2(sS[s * C::S_STAGE + soff + (B_MN ? 0 : (it & 7) * 2)]);
             const bool in_k = B_MN || it * BK + (unit0 >> 2) * 32 < args.K;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint4 v = valid && in_k ? decode8_mx4(ws[u], scale2) : make_uint4(0, 0, 0, 0);
-              st_shared_v4(b + (((unit0 + u) ^ (srow & 7)) << 4), v);
-            }
+            decode_block_mx4(ws, sS[s * C::S_STAGE + soff + (B_MN ? 0 : (it & 7) * 2)], valid && in_k, b, unit0,
+                             srow & 7);
           } else {
             const float am = reinterpret_cast<const float*>(sS + s * C::S_STAGE)[soff + (B_MN ? 0 : (it & 3))];
 #pragma unroll

@@ -60,6 +60,8 @@ extern "C" soup_status soup_linear_fwd(const soup_weight* W, const uint16_t* x, 
   if (T == 0) return SOUP_OK;
   if (W->kind == SOUP_WEIGHT_MXFP4 && T <= MX4_FEW_TOKENS)
     return mx4_few(W, x, ldx, (int)T, y, ldy, static_cast<cudaStream_t>(stream));
+  if (W->kind == SOUP_WEIGHT_MXFP4 && T <= 1024)
+    return mx4_mid(W, false, x, ldx, (int)T, y, ldy, static_cast<cudaStream_t>(stream));
   GemmDesc g;
   g.M = (int)T; g.N = (int)W->out_features; g.K = (int)W->in_features;
   g.A = Mat{x, T, W->in_features, ldx};
@@ -74,6 +76,8 @@ extern "C" soup_status soup_linear_bwd(const soup_weight* W, const uint16_t* dy,
   SOUP_TRY(check_linear("soup_linear_bwd", W, dy, lddy, W ? W->out_features : 0, T, dx, lddx, W ? W->in_features : 0,
                         workspace, workspace_bytes));
   if (T == 0) return SOUP_OK;
+  if (W->kind == SOUP_WEIGHT_MXFP4 && T <= 1024)
+    return mx4_mid(W, true, dy, lddy, (int)T, dx, lddx, static_cast<cudaStream_t>(stream));
   GemmDesc g;
   g.M = (int)T; g.N = (int)W->in_features; g.K = (int)W->out_features;
   g.A = Mat{dy, T, W->out_features, lddy};

@@ -10,4 +10,8 @@ constexpr int MX4_FEW_TOKENS = 32;
 soup_status mx4_few(const soup_weight* W, const uint16_t* x, int64_t ldx, int T, uint16_t* y, int64_t ldy,
                     cudaStream_t st);
 
+// The same on tcgen05, 1 <= T; trans: dx [T, in] = dy [T, out] W (x, y are dy, dx).
+soup_status mx4_mid(const soup_weight* W, bool trans, const uint16_t* x, int64_t ldx, int T, uint16_t* y, int64_t ldy,
+                    cudaStream_t st);
+
 }  // namespace soup

@@ -12,41 +12,68 @@ namespace soup {
 
 __host__ __device__ constexpr int64_t mx4_scale_stride(int64_t in) { return (in / 32 + 15) / 16 * 16; }
 
-// bf16x2 with 2^(s - 127) in both halves: the exponent field is s itself;
-// s = 0 is the subnormal 2^-127 and s = 255 a NaN.
-__device__ __forceinline__ uint32_t mx4_scale_bf16x2(uint32_t s) {
-  const uint32_t h = s == 0 ? 0x0040u : (s == 255 ? 0x7FC0u : s << 7);
-  return h * 0x00010001u;
-}
-
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
-// 8 codes (one word, element k in bits 4k..4k+3) times the block scale, as 4
-// bf16x2 words in element order.  A code's exponent and mantissa bits moved
-// to bits 8..6 of a bf16 are the value times 2^-126 (code exponent 0 lands
-// on a bf16 subnormal, which has the same meaning), so one multiplication by
-// 2^126 gives the element, and one by the scale the stored value; both are
-// exact (the value has two significant bits) down to bf16's smallest
-// subnormal, and a value beyond bf16's largest becomes infinite.  Elements k
-// and k + 4 share a word until the permutes put neighbours together.
-__device__ __forceinline__ void mx4_decode8(uint32_t w, uint32_t scale2, uint32_t (&o)[4]) {
-  constexpr uint32_t MAG = 0x01C001C0u, SGN = 0x80008000u, UP = 0x7E807E80u;  // UP: 2^126
-  uint32_t p0 = ((w << 6) & MAG) | ((w << 12) & SGN);
-  uint32_t p1 = ((w << 2) & MAG) | ((w << 8) & SGN);
-  uint32_t p2 = ((w >> 2) & MAG) | ((w << 4) & SGN);
-  uint32_t p3 = ((w >> 6) & MAG) | (w & SGN);
-  p0 = mul_bf16x2(mul_bf16x2(p0, UP), scale2);
-  p1 = mul_bf16x2(mul_bf16x2(p1, UP), scale2);
-  p2 = mul_bf16x2(mul_bf16x2(p2, UP), scale2);
-  p3 = mul_bf16x2(mul_bf16x2(p3, UP), scale2);
-  o[0] = __byte_perm(p0, p1, 0x5410);
-  o[1] = __byte_perm(p2, p3, 0x5410);
-  o[2] = __byte_perm(p0, p1, 0x7632);
-  o[3] = __byte_perm(p2, p3, 0x7632);
+// A code's exponent and mantissa bits moved to bits 8..6 of a bf16 are the
+// element times 2^-126 (code exponent 0 lands on a bf16 subnormal, which has
+// the same meaning), so that times 2^(s - 1) is the stored value; the product
+// is exact (two significant bits) down to bf16's smallest subnormal.  2^(s -
+// 1) is a bf16 up to s = 128 (scales up to 2); above, the rest of it follows
+// in a second product (mx4_large), where a value beyond bf16's largest
+// becomes infinite and s = 255 gives NaN.
+__device__ __forceinline__ uint32_t mx4_scale_bf16x2(uint32_t s) { return (min(s, 128u) + 126u) * 0x00800080u; }
+__device__ __forceinline__ bool mx4_is_large(uint32_t s) { return s > 128; }
+__device__ __forceinline__ uint32_t mx4_large_bf16x2(uint32_t s) {
+  return s == 255 ? 0x7FC07FC0u : (s - 1u) * 0x00800080u;  // 2^(s - 128)
+}
+
+// 8 codes (one word, element k in bits 4k..4k+3) times 2^(s - 1), as 4 bf16x2
+// words of the pairs (k, k + 4).
+__device__ __forceinline__ void mx4_decode_pairs(uint32_t w, uint32_t scale2, uint32_t (&p)[4]) {
+  constexpr uint32_t MAG = 0x01C001C0u, SGN = 0x80008000u;
+  p[0] = mul_bf16x2(((w << 6) & MAG) | ((w << 12) & SGN), scale2);
+  p[1] = mul_bf16x2(((w << 2) & MAG) | ((w << 8) & SGN), scale2);
+  p[2] = mul_bf16x2(((w >> 2) & MAG) | ((w << 4) & SGN), scale2);
+  p[3] = mul_bf16x2(((w >> 6) & MAG) | (w & SGN), scale2);
+}
+
+// A block of 32 codes (four words) with scale byte s as 16 bf16x2 words in
+// element order.
+__device__ __forceinline__ void mx4_decode_block(const uint32_t (&w)[4], uint32_t s, uint32_t (&o)[16]) {
+  const uint32_t scale2 = mx4_scale_bf16x2(s);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    uint32_t p[4];
+    mx4_decode_pairs(w[u], scale2, p);
+    o[4 * u] = __byte_perm(p[0], p[1], 0x5410);
+    o[4 * u + 1] = __byte_perm(p[2], p[3], 0x5410);
+    o[4 * u + 2] = __byte_perm(p[0], p[1], 0x7632);
+    o[4 * u + 3] = __byte_perm(p[2], p[3], 0x7632);
+  }
+  if (mx4_is_large(s)) {
+    const uint32_t more = mx4_large_bf16x2(s);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = mul_bf16x2(o[i], more);
+  }
+}
+
+// One word of such a block.
+__device__ __forceinline__ void mx4_decode8(uint32_t w, uint32_t s, uint32_t (&o)[4]) {
+  uint32_t p[4];
+  mx4_decode_pairs(w, mx4_scale_bf16x2(s), p);
+  o[0] = __byte_perm(p[0], p[1], 0x5410);
+  o[1] = __byte_perm(p[2], p[3], 0x5410);
+  o[2] = __byte_perm(p[0], p[1], 0x7632);
+  o[3] = __byte_perm(p[2], p[3], 0x7632);
+  if (mx4_is_large(s)) {
+    const uint32_t more = mx4_large_bf16x2(s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = mul_bf16x2(o[i], more);
+  }
 }
 
 }  // namespace soup

@@ -33,15 +33,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The 8 codes of a word as 4 bf16x2 pairs (k, k + 4) times the scale.
-__device__ __forceinline__ void decode_pairs(uint32_t w, uint32_t scale2, uint32_t (&p)[4]) {
-  constexpr uint32_t MAG = 0x01C001C0u, SGN = 0x80008000u, UP = 0x7E807E80u;  // as in mx4_decode8
-  p[0] = mul_bf16x2(mul_bf16x2(((w << 6) & MAG) | ((w << 12) & SGN), UP), scale2);
-  p[1] = mul_bf16x2(mul_bf16x2(((w << 2) & MAG) | ((w << 8) & SGN), UP), scale2);
-  p[2] = mul_bf16x2(mul_bf16x2(((w >> 2) & MAG) | ((w << 4) & SGN), UP), scale2);
-  p[3] = mul_bf16x2(mul_bf16x2(((w >> 6) & MAG) | (w & SGN), UP), scale2);
-}
-
 // MT: 16-row groups of W per CTA; NT: groups of 8 tokens; DEPTH: turns whose
 // loads of W are in flight together.
 template <int MT, int NT, int DEPTH>
@@ -79,8 +70,12 @@ __global__ void __launch_bounds__(32 * WARPS) mx4_few_kernel(const uint8_t* __re
       const int b = (turn0 + d * WARPS) * 4 + tq;
       if (turn0 + d * WARPS >= turns) break;
       uint32_t sc[2 * MT];
+      bool large = false;  // rare: a scale above 2
 #pragma unroll
-      for (int r = 0; r < 2 * MT; ++r) sc[r] = mx4_scale_bf16x2(s[d][r]);
+      for (int r = 0; r < 2 * MT; ++r) {
+        sc[r] = mx4_scale_bf16x2(s[d][r]);
+        large |= mx4_is_large(s[d][r]);
+      }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         uint32_t bx[NT][4];
@@ -98,8 +93,17 @@ __global__ void __launch_bounds__(32 * WARPS) mx4_few_kernel(const uint8_t* __re
         for (int i = 0; i < MT; ++i) {
           const uint4 lo = w[d][2 * i], hi = w[d][2 * i + 1];
           uint32_t p[4], q[4];
-          decode_pairs(u == 0 ? lo.x : u == 1 ? lo.y : u == 2 ? lo.z : lo.w, sc[2 * i], p);
-          decode_pairs(u == 0 ? hi.x : u == 1 ? hi.y : u == 2 ? hi.z : hi.w, sc[2 * i + 1], q);
+          mx4_decode_pairs(u == 0 ? lo.x : u == 1 ? lo.y : u == 2 ? lo.z : lo.w, sc[2 * i], p);
+          mx4_decode_pairs(u == 0 ? hi.x : u == 1 ? hi.y : u == 2 ? hi.z : hi.w, sc[2 * i + 1], q);
+          if (large) {
+            const uint32_t more[2] = {mx4_is_large(s[d][2 * i]) ? mx4_large_bf16x2(s[d][2 * i]) : 0x3F803F80u,
+                                      mx4_is_large(s[d][2 * i + 1]) ? mx4_large_bf16x2(s[d][2 * i + 1]) : 0x3F803F80u};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              p[k] = mul_bf16x2(p[k], more[0]);
+              q[k] = mul_bf16x2(q[k], more[1]);
+            }
+          }
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             mma16816(acc[i][j], p[0], q[0], p[1], q[1], bx[j][0], bx[j][1]);

@@ -1,0 +1,342 @@
+// The frozen MXFP4 product for some dozens to some hundreds of tokens, on
+// tcgen05 with the weights as the M side: D[128 weight rows, tokens] per CTA,
+//   forward   y^T = W x^T     A = W rows, K-major            (K = in)
+//   backward  dx^T = W^T dy^T A = W columns, MN-major        (K = out)
+//
+// The GEMM engine's tiles have 256 tokens by 256 weight rows per CTA pair:
+// with few tokens most of a tile is padding, and a projection has too few
+// tiles for the GPU.  With the tokens as N the tile is as wide as T needs (16
+// to 256 columns), and K is cut over a cluster of up to 8 CTAs, so that
+// tiles times slices is about the number of SMs.  The slices' sums meet in
+// distributed shared memory: every CTA leaves its fp32 partial in its own
+// shared memory and finishes a share of the tokens, adding the partials in
+// slice order (the same bits on every run, no workspace, no second launch).
+//
+// Warps: 0 TMA of the x tiles, 1 MMA, 2 TMA of codes and scales, 3..18 decode:
+// two groups of 8 take k-blocks in turn; each thread turns one block of 32
+// codes into bf16 and stores it in the swizzled A stage.
+
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "linear.h"
+#include "mx4.cuh"
+#include "ptx.cuh"
+
+namespace soup {
+namespace {
+
+constexpr int ROWS = 128;             // weight rows (columns) per CTA
+constexpr int A_BYTES = ROWS * 128;   // one 64-wide k-block of A
+constexpr int GROUPS = 2;             // decode groups of 8 warps, k-blocks in turn
+constexpr int THREADS = 32 * (3 + 8 * GROUPS);
+constexpr int MAX_STAGES = 8;
+// Codes come CODE_KB k-blocks at a time: 128 rows x 128 bytes (swizzled) and
+// 16 scale bytes per row (of 8 k-blocks, two loads' worth), or 256 k-rows x
+// 64 bytes and 16 scale bytes per k-row.
+constexpr int CODE_KB = 4, CODE_SLOTS = 3;
+constexpr int CODE_BYTES = 16384, SCALE_BYTES = 2048, SCALE_BYTES_T = 4096;
+constexpr int BAR_BYTES = 256;
+
+struct MidArgs {
+  int M, K, T;        // M: outputs per token; K: summed
+  int bn;             // tokens per tile, a multiple of 16
+  int stages, slices;
+  uint16_t* y;
+  int64_t ldy;
+  int* err;
+  long long wait_limit;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+#define MID_WAIT(bar, parity)                                              \
+  (ptx::mbar_wait_warp((bar), (parity), abort_flag, a.wait_limit) ||            \
+   (atomicOr(a.err, 1), *abort_flag = 1, false))
+
+template <bool TRANS>
+__global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant__ CUtensorMap tmx,
+                                                          const __grid_constant__ CUtensorMap tmc,
+                                                          const __grid_constant__ CUtensorMap tms, const MidArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int b_bytes = a.bn * 128, stages = a.stages;
+  uint8_t* sA = sm;
+  uint8_t* sB = sm + stages * A_BYTES;
+  uint8_t* sC = sB + stages * b_bytes;
+  uint8_t* sS = sC + CODE_SLOTS * CODE_BYTES;
+  // the partial sums [bn][ROWS] fp32 take the stages' place when K is done
+  const int ring = stages * (A_BYTES + b_bytes) + CODE_SLOTS * (CODE_BYTES + SCALE_BYTES_T), parts = a.bn * ROWS * 4;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + (ring > parts ? ring : parts));
+  uint64_t* empty = full + MAX_STAGES;
+  uint64_t* cfull = empty + MAX_STAGES;
+  uint64_t* cempty = cfull + CODE_SLOTS;
+  uint64_t* accf = cempty + CODE_SLOTS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  // warp-uniform, and known to the compiler as such (see the TMA and MMA loops)
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int slice = (int)blockIdx.x % a.slices, m0 = (int)blockIdx.x / a.slices * ROWS, t0 = (int)blockIdx.y * a.bn;
+  const int num_kb = (a.K + 63) / 64;
+  // slices of whole code loads
+  const int loads = (num_kb + CODE_KB - 1) / CODE_KB;
+  const int kb0 = (int)((int64_t)slice * loads / a.slices) * CODE_KB;
+  const int kb1 = min((int)((int64_t)(slice + 1) * loads / a.slices) * CODE_KB, num_kb);
+  const int nk = kb1 - kb0;
+  const uint32_t cols = a.bn <= 32 ? 32 : (a.bn <= 64 ? 64 : (a.bn <= 128 ? 128 : 256));
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      ptx::mbar_init(&full[s], 1 + 8);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int g = 0; g < CODE_SLOTS; ++g) {
+      ptx::mbar_init(&cfull[g], 1);
+      ptx::mbar_init(&cempty[g], 8 * GROUPS);
+    }
+    ptx::mbar_init(accf, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmc);
+    ptx::prefetch_tmap(&tms);
+    ptx::prefetch_tmap(&tmx);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(tmem_slot, cols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+
+  // These three warps run their loops as a whole, and one lane issues: in a loop
+  // of a single lane every operand would pass from vector to uniform
+  // registers, and the issuing thread would set the pace.
+  if (warp == 0) {
+    const bool leader = ptx::elect_one();
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < nk; ++i) {
+      if (!MID_WAIT(&empty[s], ph ^ 1)) break;
+      if (leader) {
+        ptx::mbar_arrive_expect_tx(&full[s], (uint32_t)b_bytes);
+        ptx::tma_load_2d(sB + s * b_bytes, &tmx, &full[s], (kb0 + i) * 64, t0);
+      }
+      if (++s == stages) { s = 0; ph ^= 1; }
+    }
+  } else if (warp == 2) {
+    const bool leader = ptx::elect_one();
+    int g = 0;
+    uint32_t gph = 0;
+    for (int kb = kb0; kb < kb1; kb += CODE_KB) {
+      if (!MID_WAIT(&cempty[g], gph ^ 1)) break;
+      if (leader) {
+        ptx::mbar_arrive_expect_tx(&cfull[g], CODE_BYTES + (TRANS ? SCALE_BYTES_T : SCALE_BYTES));
+        ptx::tma_load_2d(sC + g * CODE_BYTES, &tmc, &cfull[g], TRANS ? m0 / 2 : kb * 32, TRANS ? kb * 64 : m0);
+        ptx::tma_load_2d(sS + g * SCALE_BYTES_T, &tms, &cfull[g], (TRANS ? m0 / 32 : kb * 2) & ~15,
+                         TRANS ? kb * 64 : m0);
+      }
+      if (++g == CODE_SLOTS) { g = 0; gph ^= 1; }
+    }
+  } else if (warp == 1) {
+    const bool leader = ptx::elect_one();
+    const uint32_t idesc = ptx::idesc_bf16(ROWS, a.bn, TRANS ? 1 : 0, 0);
+    constexpr uint32_t HI = ptx::desc_hi_sw128(1024);
+    constexpr uint32_t A_STEP = TRANS ? 2048 >> 4 : 2;
+    const uint32_t a0 = ptx::desc_lo(ptx::smem_u32(sA), TRANS ? 8192 : 16);
+    const uint32_t b0 = ptx::desc_lo(ptx::smem_u32(sB), 16);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int i = 0; i < nk; ++i) {
+      if (!MID_WAIT(&full[s], ph)) { ok = false; break; }
+      ptx::tc_fence_after();
+      const uint32_t alo = a0 + s * (A_BYTES >> 4), blo = b0 + s * (b_bytes >> 4);
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          ptx::mma_bf16(tmem, ptx::desc_of(alo + k * A_STEP, HI), ptx::desc_of(blo + k * 2, HI), idesc,
+                        (i > 0 || k > 0) ? 1u : 0u);
+        ptx::mma_commit(&empty[s]);
+      }
+      if (++s == stages) { s = 0; ph ^= 1; }
+    }
+    if (ok && leader) ptx::mma_commit(accf);
+  } else {
+    const int group = (warp - 3) >> 3, t = (threadIdx.x - 96) & 255;
+    // forward: row t / 2, block t % 2 of the k-block; backward: k-row t / 4,
+    // the columns' block t % 4
+    const int r = TRANS ? t >> 2 : t >> 1, h = TRANS ? t & 3 : t & 1;
+    const bool inside = TRANS ? m0 + h * 32 < a.M : m0 + r < a.M;
+    uint8_t* const dst = TRANS ? sA + (h >> 1) * 8192 + r * 128 : sA + r * 128;
+    const int unit0 = TRANS ? (h & 1) * 4 : h * 4;
+    const int s_at = r * 16 + (TRANS ? (m0 / 32 & 15) + h : h);
+    int s = group % stages, g = 0;
+    uint32_t ph = (uint32_t)(group / stages) & 1, gph = 0;
+    for (int i = group; i < nk; i += GROUPS) {
+      const int in = i % CODE_KB;  // the k-block's place in its code load
+      if (in == group && !MID_WAIT(&cfull[g], gph)) break;
+      const uint8_t* const cp = sC + g * CODE_BYTES +
+                                (TRANS ? in * 4096 + r * 64 + h * 16 : r * 128 + (((in * 2 + h) ^ (r & 7)) << 4));
+      const uint4 c = *reinterpret_cast<const uint4*>(cp);
+      uint32_t sc = sS[g * SCALE_BYTES_T + s_at + (TRANS ? in * 1024 : ((kb0 + i) & 7) * 2)];
+      uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      // beyond the matrix TMA gave zeros, but not where a row's end lies
+      // inside its padded scales
+      if (!inside || (!TRANS && (kb0 + i) * 64 + h * 32 >= a.K)) w[0] = w[1] = w[2] = w[3] = sc = 0;
+      uint32_t v[16];
+      mx4_decode_block(w, sc, v);
+      if (!MID_WAIT(&empty[s], ph ^ 1)) break;
+      uint8_t* const o = dst + s * A_BYTES;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<uint4*>(o + (((unit0 + u) ^ (r & 7)) << 4)) =
+            make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      const bool last = in + GROUPS >= CODE_KB || i + GROUPS >= nk;  // this warp is done with the slot
+      if (lane == 0) {
+        ptx::mbar_arrive(&full[s]);
+        if (last) ptx::mbar_arrive(&cempty[g]);
+      }
+      if (last && ++g == CODE_SLOTS) { g = 0; gph ^= 1; }
+      if ((s += GROUPS) >= stages) { s -= stages; ph ^= 1; }
+    }
+    // the accumulator to shared memory as [token][row]: the stages are free
+    // once every MMA has completed
+    if (MID_WAIT(accf, 0)) {
+      ptx::tc_fence_after();
+      const int q = warp & 3;
+      float* part = reinterpret_cast<float*>(sm) + q * 32 + lane;
+      for (int c = (warp - 3) >> 2; c < a.bn / 16; c += 2 * GROUPS) {
+        uint32_t v[16];
+        ptx::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c * 16, v);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) part[(c * 16 + k) * ROWS] = __uint_as_float(v[k]);
+      }
+    }
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  if (*abort_flag) {
+    // let copies and MMAs already in flight land (bounded: about 1 ms)
+    const long long c0 = clock64();
+    while (clock64() - c0 < 2000000LL) {
+    }
+  }
+  if (a.slices > 1) ptx::cluster_sync();
+  if (!*abort_flag) {
+    // this CTA's share of the tile's tokens: the slices' partials in order
+    const int per = (a.bn + a.slices - 1) / a.slices;
+    const uint32_t base = ptx::smem_u32(sm) + lane * 16;
+    const int m = m0 + lane * 4;
+    for (int t = slice * per + warp; t < min((slice + 1) * per, a.bn); t += THREADS / 32) {
+      if (t0 + t >= a.T) break;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p = 0; p < a.slices; ++p) {
+        const uint32_t at = base + t * ROWS * 4;
+        const float4 x = ld_cluster_f4(a.slices > 1 ? ptx::mapa_shared(at, p) : at);
+        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+      }
+      if (m < a.M) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(a.y + (int64_t)(t0 + t) * a.ldy + m) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
+    }
+  }
+  if (a.slices > 1) ptx::cluster_sync();  // no CTA leaves while another reads its partial
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, cols);
+  }
+}
+
+constexpr int CU_U8 = 0, CU_BF16 = 9;  // CU_TENSOR_MAP_DATA_TYPE_*
+constexpr int CU_SWIZZLE_128 = 3;
+
+soup_status make_map(CUtensorMap* m, const void* p, int type, int64_t cols, int64_t rows, int64_t row_bytes,
+                     uint32_t box_cols, uint32_t box_rows, int swizzle, const char* what) {
+  EncodeTiledFn enc = encode_tiled();
+  SOUP_CHECK(enc != nullptr, SOUP_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const uint64_t gdim[2] = {(uint64_t)cols, (uint64_t)rows}, gstride[1] = {(uint64_t)row_bytes};
+  const uint32_t box[2] = {box_cols, box_rows}, estr[2] = {1, 1};
+  const int r = enc(m, type, 2, const_cast<void*>(p), gdim, gstride, box, estr, 0, swizzle, 3 /* L2 promotion 256 B */, 0);
+  SOUP_CHECK(r == 0, SOUP_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, r);
+  return SOUP_OK;
+}
+
+template <bool TRANS>
+soup_status launch_mid(const CUtensorMap (&map)[3], const MidArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
+  auto kern = mx4_mid_kernel<TRANS>;
+  SOUP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448));
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.slices;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  SOUP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, map[0], map[1], map[2], a));
+  SOUP_LAUNCH_CHECK();
+  return SOUP_OK;
+}
+
+}  // namespace
+
+soup_status mx4_mid(const soup_weight* W, bool trans, const uint16_t* x, int64_t ldx, int T, uint16_t* y, int64_t ldy,
+                    cudaStream_t st) {
+  MidArgs a;
+  memset(&a, 0, sizeof(a));
+  a.M = (int)(trans ? W->in_features : W->out_features);
+  a.K = (int)(trans ? W->out_features : W->in_features);
+  a.T = T;
+  a.y = y;
+  a.ldy = ldy;
+  const int ttiles = (T + 255) / 256;
+  a.bn = ((T + ttiles - 1) / ttiles + 15) / 16 * 16;
+  const int rtiles = (a.M + ROWS - 1) / ROWS, num_kb = (a.K + 63) / 64;
+  a.slices = 1;
+  while (a.slices < 8 && rtiles * ttiles * a.slices * 2 <= sm_count() && num_kb / (a.slices * 2) >= CODE_KB) a.slices *= 2;
+  a.err = device_error_word();
+  SOUP_CHECK(a.err != nullptr, SOUP_ERR_CUDA, "device error word unavailable");
+  a.wait_limit = 4000000000LL;
+  const int stage = A_BYTES + a.bn * 128, rest = CODE_SLOTS * (CODE_BYTES + SCALE_BYTES_T);
+  a.stages = std::min(MAX_STAGES, (232448 - 1024 - BAR_BYTES - rest) / stage);
+  const size_t smem = 1024 + std::max(a.stages * stage + rest, a.bn * ROWS * 4) + BAR_BYTES;
+  CUtensorMap map[3];
+  const int64_t out = W->out_features, in = W->in_features;
+  SOUP_TRY(make_map(&map[0], x, CU_BF16, a.K, T, ldx * 2, 64, (uint32_t)a.bn, CU_SWIZZLE_128, "x"));
+  SOUP_TRY(make_map(&map[1], W->codes, CU_U8, in / 2, out, in / 2, trans ? 64 : 128, trans ? 256 : 128,
+                    trans ? 0 : CU_SWIZZLE_128, "codes"));
+  SOUP_TRY(make_map(&map[2], W->scales, CU_U8, mx4_scale_stride(in), out, mx4_scale_stride(in), 16,
+                    trans ? 256 : 128, 0, "scales"));
+  const double n = (double)W->out_features * W->in_features;
+  profile_begin(st, trans ? GC_NF4_BWD : GC_NF4_FWD, 2.0 * T * n,
+                n * (0.5 + 1.0 / 32) + 2.0 * T * (W->out_features + W->in_features));
+  const dim3 grid(rtiles * a.slices, ttiles);
+  if (trans) SOUP_TRY(launch_mid<true>(map, a, grid, smem, st));
+  else SOUP_TRY(launch_mid<false>(map, a, grid, smem, st));
+  profile_end(st);
+  return SOUP_OK;
+}
+
+}  // namespace soup

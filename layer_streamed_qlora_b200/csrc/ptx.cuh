@@ -77,6 +77,13 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// The same by a whole converged warp: one answer for all lanes, which also
+// keeps them within a phase of each other.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                               long long limit_cycles = 4000000000LL) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, limit_cycles));
+}
+
 // ------------------------------------------------- CTA pairs (2-CTA clusters)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
@@ -284,6 +291,28 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+
+// One lane of a converged warp (the same one on every call).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// The two words of smem_desc_sw128's descriptor.  An issuing loop keeps the
+// upper one and adds (bytes >> 4) to the lower one per stage and k-step:
+// building descriptors in place cost an issuing thread several hundred cycles
+// per k-block.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr >> 4) & 0x3FFF) | ((lbo_bytes >> 4) & 0x3FFF) << 16;
+}
+__host__ __device__ constexpr uint32_t desc_hi_sw128(uint32_t sbo_bytes) {
+  return ((sbo_bytes >> 4) & 0x3FFF) | 1u << 14 | 2u << 29;
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
 
 // Shared-memory matrix descriptor (tcgen05): start>>4 in [0,14), leading byte
 // offset>>4 in [16,30), stride byte offset>>4 in [32,46), version 1 in
