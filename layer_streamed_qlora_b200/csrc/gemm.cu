@@ -266,7 +266,7 @@ __device__ __forceinline__ void decode_block_mx4(const uint32_t (&codes)[4], uin
   uint32_t w[4], v[16];
 #pragma unroll
   for (int u = 0; u < 4; ++u) w[u] = valid ? codes[u] : 0u;
-  mx4_decode_block(w, valid ? scale : 0u, v);
+  mx4_decode<4>(w, valid ? scale : 0u, v);
 #pragma unroll
   for (int u = 0; u < 4; ++u)
     st_shared_v4(row + (((unit0 + u) ^ swz) << 4), make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));

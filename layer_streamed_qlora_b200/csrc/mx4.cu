@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const void* __restric
       for (int64_t p = units_per_row / 4; p < scale_stride; ++p) scales[row * scale_stride + p] = 0;
     if (values) {
       uint32_t o[4];
-      mx4_decode8(code, s, o);
+      mx4_decode<1>(&code, s, o);
       values[u] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(256) mx4_dequant_kernel(const uint32_t* __rest
     const uint32_t u = (uint32_t)u64;
     const uint32_t row = u / units_per_row, c = u - row * units_per_row;
     uint32_t o[4];
-    mx4_decode8(codes[u], scales[row * scale_stride + (c >> 2)], o);
+    const uint32_t w = codes[u];
+    mx4_decode<1>(&w, scales[row * scale_stride + (c >> 2)], o);
     out[u] = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }

@@ -31,48 +31,30 @@ __device__ __forceinline__ uint32_t mx4_large_bf16x2(uint32_t s) {
   return s == 255 ? 0x7FC07FC0u : (s - 1u) * 0x00800080u;  // 2^(s - 128)
 }
 
-// 8 codes (one word, element k in bits 4k..4k+3) times 2^(s - 1), as 4 bf16x2
-// words of the pairs (k, k + 4).
-__device__ __forceinline__ void mx4_decode_pairs(uint32_t w, uint32_t scale2, uint32_t (&p)[4]) {
-  constexpr uint32_t MAG = 0x01C001C0u, SGN = 0x80008000u;
-  p[0] = mul_bf16x2(((w << 6) & MAG) | ((w << 12) & SGN), scale2);
-  p[1] = mul_bf16x2(((w << 2) & MAG) | ((w << 8) & SGN), scale2);
-  p[2] = mul_bf16x2(((w >> 2) & MAG) | ((w << 4) & SGN), scale2);
-  p[3] = mul_bf16x2(((w >> 6) & MAG) | (w & SGN), scale2);
+// 8 codes (one word, element k in bits 4k..4k+3) times `scale2` as 4 bf16x2
+// words in element order.  A product with two powers of two makes two copies
+// of a byte at once: the masks then find both codes' exponents and mantissas
+// (copies 6 and 18 up) and both signs (12 and 24 up) in place, without
+// permutes, and half of the work is the multiplier's.  (With shifts for pairs
+// (k, k + 4) and permutes after, the decode was bound by the integer pipe.)
+__device__ __forceinline__ void mx4_decode8_scaled(uint32_t w, uint32_t scale2, uint32_t* o) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t b = __byte_perm(w, 0, 0x4440 + j);
+    o[j] = mul_bf16x2(((b * 0x00040040u) & 0x01C001C0u) | ((b * 0x01001000u) & 0x80008000u), scale2);
+  }
 }
 
-// A block of 32 codes (four words) with scale byte s as 16 bf16x2 words in
-// element order.
-__device__ __forceinline__ void mx4_decode_block(const uint32_t (&w)[4], uint32_t s, uint32_t (&o)[16]) {
+// N words of one block (scale byte s).
+template <int N>
+__device__ __forceinline__ void mx4_decode(const uint32_t* w, uint32_t s, uint32_t* o) {
   const uint32_t scale2 = mx4_scale_bf16x2(s);
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    uint32_t p[4];
-    mx4_decode_pairs(w[u], scale2, p);
-    o[4 * u] = __byte_perm(p[0], p[1], 0x5410);
-    o[4 * u + 1] = __byte_perm(p[2], p[3], 0x5410);
-    o[4 * u + 2] = __byte_perm(p[0], p[1], 0x7632);
-    o[4 * u + 3] = __byte_perm(p[2], p[3], 0x7632);
-  }
+  for (int u = 0; u < N; ++u) mx4_decode8_scaled(w[u], scale2, o + 4 * u);
   if (mx4_is_large(s)) {
     const uint32_t more = mx4_large_bf16x2(s);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = mul_bf16x2(o[i], more);
-  }
-}
-
-// One word of such a block.
-__device__ __forceinline__ void mx4_decode8(uint32_t w, uint32_t s, uint32_t (&o)[4]) {
-  uint32_t p[4];
-  mx4_decode_pairs(w, mx4_scale_bf16x2(s), p);
-  o[0] = __byte_perm(p[0], p[1], 0x5410);
-  o[1] = __byte_perm(p[2], p[3], 0x5410);
-  o[2] = __byte_perm(p[0], p[1], 0x7632);
-  o[3] = __byte_perm(p[2], p[3], 0x7632);
-  if (mx4_is_large(s)) {
-    const uint32_t more = mx4_large_bf16x2(s);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = mul_bf16x2(o[i], more);
+    for (int i = 0; i < 4 * N; ++i) o[i] = mul_bf16x2(o[i], more);
   }
 }
 

@@ -10,10 +10,9 @@
 // through shared memory, nothing is split across CTAs, and the order of the
 // sums does not depend on the launch.
 //
-// The order of k inside a turn is free as long as both operands agree, so a
-// thread's four k of one instruction are those that its codes decode to
-// without permutes: of 8 neighbouring codes the pairs (0, 4), (1, 5) and then
-// (2, 6), (3, 7).  x is permuted to match when it is loaded.
+// The order of k inside a turn is free as long as both operands agree: of 8
+// neighbouring codes of a thread, the first four and then the last four are
+// its four k of one instruction, and x is read in the same order.
 #include <algorithm>
 
 #include "linear.h"
@@ -84,17 +83,17 @@ __global__ void __launch_bounds__(32 * WARPS) mx4_few_kernel(const uint8_t* __re
           const int t = 8 * j + g;
           uint4 v = make_uint4(0, 0, 0, 0);
           if (t < T && b < blocks) v = __ldg(reinterpret_cast<const uint4*>(x + t * ldx + (int64_t)b * 32) + u);
-          bx[j][0] = __byte_perm(v.x, v.z, 0x5410);
-          bx[j][1] = __byte_perm(v.x, v.z, 0x7632);
-          bx[j][2] = __byte_perm(v.y, v.w, 0x5410);
-          bx[j][3] = __byte_perm(v.y, v.w, 0x7632);
+          bx[j][0] = v.x;
+          bx[j][1] = v.y;
+          bx[j][2] = v.z;
+          bx[j][3] = v.w;
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           const uint4 lo = w[d][2 * i], hi = w[d][2 * i + 1];
           uint32_t p[4], q[4];
-          mx4_decode_pairs(u == 0 ? lo.x : u == 1 ? lo.y : u == 2 ? lo.z : lo.w, sc[2 * i], p);
-          mx4_decode_pairs(u == 0 ? hi.x : u == 1 ? hi.y : u == 2 ? hi.z : hi.w, sc[2 * i + 1], q);
+          mx4_decode8_scaled(u == 0 ? lo.x : u == 1 ? lo.y : u == 2 ? lo.z : lo.w, sc[2 * i], p);
+          mx4_decode8_scaled(u == 0 ? hi.x : u == 1 ? hi.y : u == 2 ? hi.z : hi.w, sc[2 * i + 1], q);
           if (large) {
             const uint32_t more[2] = {mx4_is_large(s[d][2 * i]) ? mx4_large_bf16x2(s[d][2 * i]) : 0x3F803F80u,
                                       mx4_is_large(s[d][2 * i + 1]) ? mx4_large_bf16x2(s[d][2 * i + 1]) : 0x3F803F80u};

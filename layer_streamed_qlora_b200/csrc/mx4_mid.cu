@@ -13,8 +13,10 @@
 // slice order (the same bits on every run, no workspace, no second launch).
 //
 // Warps: 0 TMA of the x tiles, 1 MMA, 2 TMA of codes and scales, 3..18 decode:
-// two groups of 8 take k-blocks in turn; each thread turns one block of 32
-// codes into bf16 and stores it in the swizzled A stage.
+// four groups of 4, one for each of the four k-blocks of a code load; a thread
+// turns two blocks of 32 codes into bf16 and stores them in the swizzled A
+// stage.  Decoding bounds the kernel up to some 128 tokens, by instructions:
+// two blocks per thread share its waits, fences and addresses.
 
 #include <cuda.h>
 
@@ -30,20 +32,24 @@ namespace {
 
 constexpr int ROWS = 128;             // weight rows (columns) per CTA
 constexpr int A_BYTES = ROWS * 128;   // one 64-wide k-block of A
-constexpr int GROUPS = 2;             // decode groups of 8 warps, k-blocks in turn
-constexpr int THREADS = 32 * (3 + 8 * GROUPS);
-constexpr int MAX_STAGES = 8;
+constexpr int MAX_STAGES = 8;  // of the A ring and of the x ring
 // Codes come CODE_KB k-blocks at a time: 128 rows x 128 bytes (swizzled) and
 // 16 scale bytes per row (of 8 k-blocks, two loads' worth), or 256 k-rows x
 // 64 bytes and 16 scale bytes per k-row.
 constexpr int CODE_KB = 4, CODE_SLOTS = 3;
+constexpr int GROUP_WARPS = 4;  // decode warps per k-block of a code load
+// A decode group that waits for the stage of k-block i has waited for the one
+// of k-block i - CODE_KB before.  The wait's parity tells this phase from the
+// one before only if that one is over: i - CODE_KB - stages >= i - 2 stages.
+constexpr int MIN_A_STAGES = CODE_KB;
+constexpr int THREADS = 32 * (3 + GROUP_WARPS * CODE_KB);
 constexpr int CODE_BYTES = 16384, SCALE_BYTES = 2048, SCALE_BYTES_T = 4096;
-constexpr int BAR_BYTES = 256;
+constexpr int BAR_BYTES = 512;
 
 struct MidArgs {
   int M, K, T;        // M: outputs per token; K: summed
   int bn;             // tokens per tile, a multiple of 16
-  int stages, slices;
+  int a_stages, x_stages, slices;
   uint16_t* y;
   int64_t ldy;
   int* err;
@@ -59,6 +65,22 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t* v) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
 #define MID_WAIT(bar, parity)                                              \
   (ptx::mbar_wait_warp((bar), (parity), abort_flag, a.wait_limit) ||            \
    (atomicOr(a.err, 1), *abort_flag = 1, false))
@@ -69,16 +91,18 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
                                                           const __grid_constant__ CUtensorMap tms, const MidArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int b_bytes = a.bn * 128, stages = a.stages;
+  const int b_bytes = a.bn * 128, a_stages = a.a_stages, x_stages = a.x_stages;
   uint8_t* sA = sm;
-  uint8_t* sB = sm + stages * A_BYTES;
-  uint8_t* sC = sB + stages * b_bytes;
+  uint8_t* sB = sA + a_stages * A_BYTES;
+  uint8_t* sC = sB + x_stages * b_bytes;
   uint8_t* sS = sC + CODE_SLOTS * CODE_BYTES;
   // the partial sums [bn][ROWS] fp32 take the stages' place when K is done
-  const int ring = stages * (A_BYTES + b_bytes) + CODE_SLOTS * (CODE_BYTES + SCALE_BYTES_T), parts = a.bn * ROWS * 4;
+  const int ring = a_stages * A_BYTES + x_stages * b_bytes + CODE_SLOTS * (CODE_BYTES + SCALE_BYTES_T), parts = a.bn * ROWS * 4;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + (ring > parts ? ring : parts));
   uint64_t* empty = full + MAX_STAGES;
-  uint64_t* cfull = empty + MAX_STAGES;
+  uint64_t* xfull = empty + MAX_STAGES;
+  uint64_t* xempty = xfull + MAX_STAGES;
+  uint64_t* cfull = xempty + MAX_STAGES;
   uint64_t* cempty = cfull + CODE_SLOTS;
   uint64_t* accf = cempty + CODE_SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
@@ -96,13 +120,15 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
   const uint32_t cols = a.bn <= 32 ? 32 : (a.bn <= 64 ? 64 : (a.bn <= 128 ? 128 : 256));
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      ptx::mbar_init(&full[s], 1 + 8);
+    for (int s = 0; s < MAX_STAGES; ++s) {
+      ptx::mbar_init(&full[s], GROUP_WARPS);
       ptx::mbar_init(&empty[s], 1);
+      ptx::mbar_init(&xfull[s], 1);
+      ptx::mbar_init(&xempty[s], 1);
     }
     for (int g = 0; g < CODE_SLOTS; ++g) {
       ptx::mbar_init(&cfull[g], 1);
-      ptx::mbar_init(&cempty[g], 8 * GROUPS);
+      ptx::mbar_init(&cempty[g], GROUP_WARPS * CODE_KB);
     }
     ptx::mbar_init(accf, 1);
     *abort_flag = 0;
@@ -128,12 +154,12 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
     int s = 0;
     uint32_t ph = 0;
     for (int i = 0; i < nk; ++i) {
-      if (!MID_WAIT(&empty[s], ph ^ 1)) break;
+      if (!MID_WAIT(&xempty[s], ph ^ 1)) break;
       if (leader) {
-        ptx::mbar_arrive_expect_tx(&full[s], (uint32_t)b_bytes);
-        ptx::tma_load_2d(sB + s * b_bytes, &tmx, &full[s], (kb0 + i) * 64, t0);
+        ptx::mbar_arrive_expect_tx(&xfull[s], (uint32_t)b_bytes);
+        ptx::tma_load_2d(sB + s * b_bytes, &tmx, &xfull[s], (kb0 + i) * 64, t0);
       }
-      if (++s == stages) { s = 0; ph ^= 1; }
+      if (++s == x_stages) { s = 0; ph ^= 1; }
     }
   } else if (warp == 2) {
     const bool leader = ptx::elect_one();
@@ -156,62 +182,68 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
     constexpr uint32_t A_STEP = TRANS ? 2048 >> 4 : 2;
     const uint32_t a0 = ptx::desc_lo(ptx::smem_u32(sA), TRANS ? 8192 : 16);
     const uint32_t b0 = ptx::desc_lo(ptx::smem_u32(sB), 16);
-    int s = 0;
-    uint32_t ph = 0;
+    int s = 0, xs = 0;
+    uint32_t ph = 0, xph = 0;
     bool ok = true;
     for (int i = 0; i < nk; ++i) {
-      if (!MID_WAIT(&full[s], ph)) { ok = false; break; }
+      if (!MID_WAIT(&xfull[xs], xph) || !MID_WAIT(&full[s], ph)) { ok = false; break; }
       ptx::tc_fence_after();
-      const uint32_t alo = a0 + s * (A_BYTES >> 4), blo = b0 + s * (b_bytes >> 4);
+      const uint32_t alo = a0 + s * (A_BYTES >> 4), blo = b0 + xs * (b_bytes >> 4);
       if (leader) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           ptx::mma_bf16(tmem, ptx::desc_of(alo + k * A_STEP, HI), ptx::desc_of(blo + k * 2, HI), idesc,
                         (i > 0 || k > 0) ? 1u : 0u);
         ptx::mma_commit(&empty[s]);
+        ptx::mma_commit(&xempty[xs]);
       }
-      if (++s == stages) { s = 0; ph ^= 1; }
+      if (++s == a_stages) { s = 0; ph ^= 1; }
+      if (++xs == x_stages) { xs = 0; xph ^= 1; }
     }
     if (ok && leader) ptx::mma_commit(accf);
   } else {
-    const int group = (warp - 3) >> 3, t = (threadIdx.x - 96) & 255;
-    // forward: row t / 2, block t % 2 of the k-block; backward: k-row t / 4,
-    // the columns' block t % 4
-    const int r = TRANS ? t >> 2 : t >> 1, h = TRANS ? t & 3 : t & 1;
-    const bool inside = TRANS ? m0 + h * 32 < a.M : m0 + r < a.M;
-    uint8_t* const dst = TRANS ? sA + (h >> 1) * 8192 + r * 128 : sA + r * 128;
-    const int unit0 = TRANS ? (h & 1) * 4 : h * 4;
-    const int s_at = r * 16 + (TRANS ? (m0 / 32 & 15) + h : h);
-    int s = group % stages, g = 0;
-    uint32_t ph = (uint32_t)(group / stages) & 1, gph = 0;
-    for (int i = group; i < nk; i += GROUPS) {
-      const int in = i % CODE_KB;  // the k-block's place in its code load
-      if (in == group && !MID_WAIT(&cfull[g], gph)) break;
-      const uint8_t* const cp = sC + g * CODE_BYTES +
-                                (TRANS ? in * 4096 + r * 64 + h * 16 : r * 128 + (((in * 2 + h) ^ (r & 7)) << 4));
-      const uint4 c = *reinterpret_cast<const uint4*>(cp);
-      uint32_t sc = sS[g * SCALE_BYTES_T + s_at + (TRANS ? in * 1024 : ((kb0 + i) & 7) * 2)];
-      uint32_t w[4] = {c.x, c.y, c.z, c.w};
-      // beyond the matrix TMA gave zeros, but not where a row's end lies
-      // inside its padded scales
-      if (!inside || (!TRANS && (kb0 + i) * 64 + h * 32 >= a.K)) w[0] = w[1] = w[2] = w[3] = sc = 0;
-      uint32_t v[16];
-      mx4_decode_block(w, sc, v);
+    // forward: weight row t, its 64 codes of the group's k-block; backward:
+    // k-row t / 2 of it, 64 of the 128 columns
+    const int group = (warp - 3) / GROUP_WARPS, t = (threadIdx.x - 96) & 127;
+    const int r = TRANS ? t >> 1 : t, h = TRANS ? t & 1 : 0;
+    const uint32_t dst = ptx::smem_u32(TRANS ? sA + h * 8192 + r * 128 : sA + r * 128) ^ ((r & 7) << 4);
+    // its two 16-byte units of codes (128-byte swizzled rows in the forward)
+    const uint32_t c0 = ptx::smem_u32(sC) + (TRANS ? group * 4096 + r * 64 + h * 32 : r * 128 + (((group * 2) ^ (r & 7)) << 4));
+    const uint32_t c1 = c0 ^ 16;
+    // its two scale bytes: a window of 16 holds 8 k-blocks, two code loads' worth
+    const uint32_t s0 = ptx::smem_u32(sS) + (TRANS ? (group * 64 + r) * 16 + (m0 / 32 & 15) + h * 2 : r * 16 + group * 2);
+    // TMA reads zeros beyond the matrix, but a row can end inside its padded
+    // scales: blocks from `blocks` on are none
+    const int blocks = TRANS ? (a.M - m0 - h * 64 + 31) / 32 : (m0 + r < a.M ? a.K / 32 : 0);
+    int s = group, g = 0;
+    uint32_t ph = 0, gph = 0;
+    for (int kb = kb0; kb + group < kb1; kb += CODE_KB) {
+      if (!MID_WAIT(&cfull[g], gph)) break;
+      uint32_t w[8], v[32];
+      ld_shared_v4(c0 + g * CODE_BYTES, w);
+      ld_shared_v4(c1 + g * CODE_BYTES, w + 4);
+      uint32_t sc = ld_shared_u16(s0 + g * SCALE_BYTES_T + (TRANS ? 0 : (kb & 4) * 2));
+      const int left = TRANS ? blocks : blocks - (kb + group) * 2;
+      if (left < 2) {
+        w[4] = w[5] = w[6] = w[7] = 0;
+        sc &= 0xFF;
+        if (left < 1) w[0] = w[1] = w[2] = w[3] = sc = 0;
+      }
+      mx4_decode<4>(w, sc & 0xFF, v);
+      mx4_decode<4>(w + 4, sc >> 8, v + 16);
       if (!MID_WAIT(&empty[s], ph ^ 1)) break;
-      uint8_t* const o = dst + s * A_BYTES;
+      const uint32_t o = dst + s * A_BYTES;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        *reinterpret_cast<uint4*>(o + (((unit0 + u) ^ (r & 7)) << 4)) =
-            make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+      for (int u = 0; u < 8; ++u) st_shared_v4(o ^ (u << 4), v + 4 * u);
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      const bool last = in + GROUPS >= CODE_KB || i + GROUPS >= nk;  // this warp is done with the slot
       if (lane == 0) {
         ptx::mbar_arrive(&full[s]);
-        if (last) ptx::mbar_arrive(&cempty[g]);
+        ptx::mbar_arrive(&cempty[g]);
       }
-      if (last && ++g == CODE_SLOTS) { g = 0; gph ^= 1; }
-      if ((s += GROUPS) >= stages) { s -= stages; ph ^= 1; }
+      if (++g == CODE_SLOTS) { g = 0; gph ^= 1; }
+      s += CODE_KB;
+      if (s >= a_stages) { s -= a_stages; ph ^= 1; }
     }
     // the accumulator to shared memory as [token][row]: the stages are free
     // once every MMA has completed
@@ -219,7 +251,7 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
       ptx::tc_fence_after();
       const int q = warp & 3;
       float* part = reinterpret_cast<float*>(sm) + q * 32 + lane;
-      for (int c = (warp - 3) >> 2; c < a.bn / 16; c += 2 * GROUPS) {
+      for (int c = (warp - 3) >> 2; c < a.bn / 16; c += CODE_KB) {
         uint32_t v[16];
         ptx::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c * 16, v);
         ptx::tmem_ld_wait();
@@ -319,9 +351,12 @@ soup_status mx4_mid(const soup_weight* W, bool trans, const uint16_t* x, int64_t
   a.err = device_error_word();
   SOUP_CHECK(a.err != nullptr, SOUP_ERR_CUDA, "device error word unavailable");
   a.wait_limit = 4000000000LL;
-  const int stage = A_BYTES + a.bn * 128, rest = CODE_SLOTS * (CODE_BYTES + SCALE_BYTES_T);
-  a.stages = std::min(MAX_STAGES, (232448 - 1024 - BAR_BYTES - rest) / stage);
-  const size_t smem = 1024 + std::max(a.stages * stage + rest, a.bn * ROWS * 4) + BAR_BYTES;
+  const int codes = CODE_SLOTS * (CODE_BYTES + SCALE_BYTES_T), room = 232448 - 1024 - BAR_BYTES - codes;
+  const int xb = a.bn * 128;
+  a.x_stages = std::min(MAX_STAGES, (room - MIN_A_STAGES * A_BYTES) / xb);  // 3 at bn = 256
+  a.a_stages = std::min(MAX_STAGES, (room - a.x_stages * xb) / A_BYTES);
+  SOUP_CHECK(a.x_stages >= 2 && a.a_stages >= MIN_A_STAGES, SOUP_ERR_SHAPE, "frozen linear: %d tokens per tile", a.bn);
+  const size_t smem = 1024 + std::max(a.a_stages * A_BYTES + a.x_stages * xb + codes, a.bn * ROWS * 4) + BAR_BYTES;
   CUtensorMap map[3];
   const int64_t out = W->out_features, in = W->in_features;
   SOUP_TRY(make_map(&map[0], x, CU_BF16, a.K, T, ldx * 2, 64, (uint32_t)a.bn, CU_SWIZZLE_128, "x"));
