@@ -1437,7 +1437,7 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
         const int s = gi % STAGES;
         const uint32_t ph = (gi / STAGES) & 1;
         // cfull completes once per use of the slot (the tail stage arrives without bytes)
-        if (!ptx::mbar_wait_bounded(&empty[s], ph ^ 1, abort_flag) ||
+        if (
             !ptx::mbar_wait_bounded(&cfull[s], ph, abort_flag)) {
           atomicOr(args.err, 1);
           *abort_flag = 1;

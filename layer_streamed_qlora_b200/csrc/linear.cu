@@ -1,10 +1,19 @@
 // The frozen projection without adapters: y = x W^T and its input gradient
-// dx = dy W (W is frozen, so there is no weight gradient), on the tcgen05
-// GEMM engine, for every storage of W.
+// dx = dy W (W is frozen, so there is no weight gradient), for every storage
+// of W.
 //
-// The engine's 256 x 256 tiles leave most of the GPU idle when T is a few
-// hundred tokens; with a workspace the tiles that do not fill a round are cut
-// along K (slices of at least 8 k-blocks), summed in slice order.
+// NF4 and bf16 weights, and MXFP4 ones with many tokens, run on the GEMM
+// engine.  Its 256 x 256 tiles leave most of the GPU idle when T is small;
+// with a workspace the tiles that do not fill a round are cut along K (slices
+// of at least 40 k-blocks: at 16 a 2048 x 512 x 1024 product took 24.7 us in
+// slices and 11.8 whole), summed in slice order.
+// MXFP4 weights with fewer tokens have kernels of their own, both measured
+// against the engine at 6144 x 4096 (us):
+//   T           1     16    33    256   512   1024   2048
+//   mx4_few     8.0   11.9  19.9 (T = 32)
+//   mx4_mid     14.8  16    16.8  22.4  32.6  62
+//   engine      37    37    37    36.5  54.7  65     113
+// so mx4_few takes up to 16 tokens of the forward, mx4_mid up to 1024.
 #include <algorithm>
 
 #include "gemm.h"
@@ -14,6 +23,7 @@
 namespace soup {
 namespace {
 
+constexpr int64_t MX4_MID_TOKENS = 1024;
 constexpr int64_t MAX_SLICES = 148;  // two per CTA pair: 37 MiB of partials at most
 
 size_t workspace_bytes_for(int64_t M, int64_t N) {
@@ -40,7 +50,7 @@ void use_workspace(GemmDesc& g, void* ws, size_t bytes) {
   g.sk_counters = static_cast<unsigned long long*>(ws);
   g.sk_scratch = static_cast<char*>(ws) + SK_COUNTER_BYTES;
   g.sk_scratch_bytes = std::min(bytes - SK_COUNTER_BYTES, (size_t)MAX_SLICES * SK_SLICE_BYTES);
-  g.sk_min_kb = 8;
+  g.sk_min_kb = 40;
 }
 
 }  // namespace
@@ -60,7 +70,7 @@ extern "C" soup_status soup_linear_fwd(const soup_weight* W, const uint16_t* x, 
   if (T == 0) return SOUP_OK;
   if (W->kind == SOUP_WEIGHT_MXFP4 && T <= MX4_FEW_TOKENS)
     return mx4_few(W, x, ldx, (int)T, y, ldy, static_cast<cudaStream_t>(stream));
-  if (W->kind == SOUP_WEIGHT_MXFP4 && T <= 1024)
+  if (W->kind == SOUP_WEIGHT_MXFP4 && T <= MX4_MID_TOKENS)
     return mx4_mid(W, false, x, ldx, (int)T, y, ldy, static_cast<cudaStream_t>(stream));
   GemmDesc g;
   g.M = (int)T; g.N = (int)W->out_features; g.K = (int)W->in_features;
@@ -76,7 +86,7 @@ extern "C" soup_status soup_linear_bwd(const soup_weight* W, const uint16_t* dy,
   SOUP_TRY(check_linear("soup_linear_bwd", W, dy, lddy, W ? W->out_features : 0, T, dx, lddx, W ? W->in_features : 0,
                         workspace, workspace_bytes));
   if (T == 0) return SOUP_OK;
-  if (W->kind == SOUP_WEIGHT_MXFP4 && T <= 1024)
+  if (W->kind == SOUP_WEIGHT_MXFP4 && T <= MX4_MID_TOKENS)
     return mx4_mid(W, true, dy, lddy, (int)T, dx, lddx, static_cast<cudaStream_t>(stream));
   GemmDesc g;
   g.M = (int)T; g.N = (int)W->in_features; g.K = (int)W->out_features;

@@ -1,6 +1,6 @@
 // y = x W^T over an MXFP4 W for few tokens.
 //
-// With T tokens a weight of 4.25 bits does 2 T flops: up to a few dozen tokens
+// With T tokens a weight of 4.25 bits does 2 T flops: up to a dozen tokens
 // the product is bound by reading W once, and the 256-wide tiles of the GEMM
 // engine leave most SMs without work.  Here W is the M side of
 // mma.sync.m16n8k16 (16 weight rows by 8 tokens): a CTA owns 16 * MT rows and
@@ -149,8 +149,7 @@ soup_status mx4_few(const soup_weight* W, const uint16_t* x, int64_t ldx, int T,
   profile_begin(st, GC_NF4_FWD, 2.0 * T * n, n * (0.5 + 1.0 / 32) + 2.0 * T * (W->out_features + W->in_features));
   soup_status r;
   if (T <= 8) r = launch_few<1, 1, 4>(W, x, ldx, T, y, ldy, st);
-  else if (T <= 16) r = launch_few<1, 2, 2>(W, x, ldx, T, y, ldy, st);
-  else r = launch_few<2, 4, 2>(W, x, ldx, T, y, ldy, st);
+  else r = launch_few<1, 2, 2>(W, x, ldx, T, y, ldy, st);
   SOUP_TRY(r);
   profile_end(st);
   return SOUP_OK;

@@ -6,7 +6,7 @@
 // The GEMM engine's tiles have 256 tokens by 256 weight rows per CTA pair:
 // with few tokens most of a tile is padding, and a projection has too few
 // tiles for the GPU.  With the tokens as N the tile is as wide as T needs (16
-// to 256 columns), and K is cut over a cluster of up to 8 CTAs, so that
+// to 256 columns), and K is cut over a cluster of up to 4 CTAs, so that
 // tiles times slices is about the number of SMs.  The slices' sums meet in
 // distributed shared memory: every CTA leaves its fp32 partial in its own
 // shared memory and finishes a share of the tokens, adding the partials in
@@ -15,8 +15,13 @@
 // Warps: 0 TMA of the x tiles, 1 MMA, 2 TMA of codes and scales, 3..18 decode:
 // four groups of 4, one for each of the four k-blocks of a code load; a thread
 // turns two blocks of 32 codes into bf16 and stores them in the swizzled A
-// stage.  Decoding bounds the kernel up to some 128 tokens, by instructions:
-// two blocks per thread share its waits, fences and addresses.
+// stage (two, to share the waits, fences and addresses).
+//
+// What bounds it: per k-block the decode takes about 330 cycles of the integer
+// pipes and the issuing lane some 350 (two barrier tries of 60 cycles, four
+// MMAs, two commits), the tensor core 2 cycles per token.  256 tokens through
+// 28672 x 4096 take 65 us (924 TFLOP/s), 64 take 49 us; the GEMM engine's
+// 256-token tiles take 84 us for either.
 
 #include <cuda.h>
 
@@ -81,9 +86,10 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t* v) {
                : "memory");
 }
 
-#define MID_WAIT(bar, parity)                                              \
-  (ptx::mbar_wait_warp((bar), (parity), abort_flag, a.wait_limit) ||            \
-   (atomicOr(a.err, 1), *abort_flag = 1, false))
+// By one lane of a warp, and by all lanes with one answer.
+#define MID_FAILED (atomicOr(a.err, 1), *abort_flag = 1, false)
+#define MID_WAIT_LANE(bar, parity) (ptx::mbar_wait_bounded((bar), (parity), abort_flag, a.wait_limit) || MID_FAILED)
+#define MID_WAIT(bar, parity) (ptx::mbar_wait_warp((bar), (parity), abort_flag, a.wait_limit) || MID_FAILED)
 
 template <bool TRANS>
 __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant__ CUtensorMap tmx,
@@ -146,61 +152,60 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
 
-  // These three warps run their loops as a whole, and one lane issues: in a loop
-  // of a single lane every operand would pass from vector to uniform
-  // registers, and the issuing thread would set the pace.
   if (warp == 0) {
-    const bool leader = ptx::elect_one();
-    int s = 0;
-    uint32_t ph = 0;
-    for (int i = 0; i < nk; ++i) {
-      if (!MID_WAIT(&xempty[s], ph ^ 1)) break;
-      if (leader) {
+    if (ptx::elect_one()) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int i = 0; i < nk; ++i) {
+        if (!MID_WAIT_LANE(&xempty[s], ph ^ 1)) break;
         ptx::mbar_arrive_expect_tx(&xfull[s], (uint32_t)b_bytes);
         ptx::tma_load_2d(sB + s * b_bytes, &tmx, &xfull[s], (kb0 + i) * 64, t0);
+        if (++s == x_stages) { s = 0; ph ^= 1; }
       }
-      if (++s == x_stages) { s = 0; ph ^= 1; }
     }
   } else if (warp == 2) {
-    const bool leader = ptx::elect_one();
-    int g = 0;
-    uint32_t gph = 0;
-    for (int kb = kb0; kb < kb1; kb += CODE_KB) {
-      if (!MID_WAIT(&cempty[g], gph ^ 1)) break;
-      if (leader) {
+    if (ptx::elect_one()) {
+      int g = 0;
+      uint32_t gph = 0;
+      for (int kb = kb0; kb < kb1; kb += CODE_KB) {
+        if (!MID_WAIT_LANE(&cempty[g], gph ^ 1)) break;
         ptx::mbar_arrive_expect_tx(&cfull[g], CODE_BYTES + (TRANS ? SCALE_BYTES_T : SCALE_BYTES));
         ptx::tma_load_2d(sC + g * CODE_BYTES, &tmc, &cfull[g], TRANS ? m0 / 2 : kb * 32, TRANS ? kb * 64 : m0);
         ptx::tma_load_2d(sS + g * SCALE_BYTES_T, &tms, &cfull[g], (TRANS ? m0 / 32 : kb * 2) & ~15,
                          TRANS ? kb * 64 : m0);
+        if (++g == CODE_SLOTS) { g = 0; gph ^= 1; }
       }
-      if (++g == CODE_SLOTS) { g = 0; gph ^= 1; }
     }
   } else if (warp == 1) {
-    const bool leader = ptx::elect_one();
-    const uint32_t idesc = ptx::idesc_bf16(ROWS, a.bn, TRANS ? 1 : 0, 0);
-    constexpr uint32_t HI = ptx::desc_hi_sw128(1024);
-    constexpr uint32_t A_STEP = TRANS ? 2048 >> 4 : 2;
-    const uint32_t a0 = ptx::desc_lo(ptx::smem_u32(sA), TRANS ? 8192 : 16);
-    const uint32_t b0 = ptx::desc_lo(ptx::smem_u32(sB), 16);
-    int s = 0, xs = 0;
-    uint32_t ph = 0, xph = 0;
-    bool ok = true;
-    for (int i = 0; i < nk; ++i) {
-      if (!MID_WAIT(&xfull[xs], xph) || !MID_WAIT(&full[s], ph)) { ok = false; break; }
-      ptx::tc_fence_after();
-      const uint32_t alo = a0 + s * (A_BYTES >> 4), blo = b0 + xs * (b_bytes >> 4);
-      if (leader) {
+    // descriptors are advanced, not built
+    if (ptx::elect_one()) {
+      const uint32_t idesc = ptx::idesc_bf16(ROWS, a.bn, TRANS ? 1 : 0, 0);
+      constexpr uint32_t HI = ptx::desc_hi_sw128(1024);
+      constexpr uint32_t A_STEP = TRANS ? 2048 >> 4 : 2;
+      const uint32_t a0 = ptx::desc_lo(ptx::smem_u32(sA), TRANS ? 8192 : 16);
+      const uint32_t b0 = ptx::desc_lo(ptx::smem_u32(sB), 16);
+      int s = 0, xs = 0;
+      uint32_t ph = 0, xph = 0;
+      bool ok = true, ready = false;
+      for (int i = 0; i < nk; ++i) {
+        if (!ready && (!MID_WAIT_LANE(&xfull[xs], xph) || !MID_WAIT_LANE(&full[s], ph))) { ok = false; break; }
+        const uint32_t alo = a0 + s * (A_BYTES >> 4), blo = b0 + xs * (b_bytes >> 4);
+        uint64_t *const done = &empty[s], *const xdone = &xempty[xs];
+        if (++s == a_stages) { s = 0; ph ^= 1; }
+        if (++xs == x_stages) { xs = 0; xph ^= 1; }
+        // the next k-block's barriers are tried before this one's MMAs are
+        // issued: a try takes 60 cycles to answer
+        const bool r0 = ptx::mbar_try_wait(&xfull[xs], xph), r1 = ptx::mbar_try_wait(&full[s], ph);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           ptx::mma_bf16(tmem, ptx::desc_of(alo + k * A_STEP, HI), ptx::desc_of(blo + k * 2, HI), idesc,
                         (i > 0 || k > 0) ? 1u : 0u);
-        ptx::mma_commit(&empty[s]);
-        ptx::mma_commit(&xempty[xs]);
+        ptx::mma_commit(done);
+        ptx::mma_commit(xdone);
+        ready = r0 && r1;
       }
-      if (++s == a_stages) { s = 0; ph ^= 1; }
-      if (++xs == x_stages) { xs = 0; xph ^= 1; }
+      if (ok) ptx::mma_commit(accf);
     }
-    if (ok && leader) ptx::mma_commit(accf);
   } else {
     // forward: weight row t, its 64 codes of the group's k-block; backward:
     // k-row t / 2 of it, 64 of the 128 columns
@@ -229,9 +234,10 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
         sc &= 0xFF;
         if (left < 1) w[0] = w[1] = w[2] = w[3] = sc = 0;
       }
+      const bool free_now = __all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(&empty[s], ph ^ 1));
       mx4_decode<4>(w, sc & 0xFF, v);
       mx4_decode<4>(w + 4, sc >> 8, v + 16);
-      if (!MID_WAIT(&empty[s], ph ^ 1)) break;
+      if (!free_now && !MID_WAIT(&empty[s], ph ^ 1)) break;
       const uint32_t o = dst + s * A_BYTES;
 #pragma unroll
       for (int u = 0; u < 8; ++u) st_shared_v4(o ^ (u << 4), v + 4 * u);
@@ -346,8 +352,10 @@ soup_status mx4_mid(const soup_weight* W, bool trans, const uint16_t* x, int64_t
   const int ttiles = (T + 255) / 256;
   a.bn = ((T + ttiles - 1) / ttiles + 15) / 16 * 16;
   const int rtiles = (a.M + ROWS - 1) / ROWS, num_kb = (a.K + 63) / 64;
+  // up to 4 slices: clusters of 8 one-per-SM CTAs do not find room at once
+  // (64 tokens through 2048 x 11008: 30 us with 8 slices, 21.5 with 4, 33 with 2)
   a.slices = 1;
-  while (a.slices < 8 && rtiles * ttiles * a.slices * 2 <= sm_count() && num_kb / (a.slices * 2) >= CODE_KB) a.slices *= 2;
+  while (a.slices < 4 && rtiles * ttiles * a.slices * 2 <= sm_count() && num_kb / (a.slices * 2) >= CODE_KB) a.slices *= 2;
   a.err = device_error_word();
   SOUP_CHECK(a.err != nullptr, SOUP_ERR_CUDA, "device error word unavailable");
   a.wait_limit = 4000000000LL;
