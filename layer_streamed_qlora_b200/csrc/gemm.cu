@@ -1208,7 +1208,7 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      ptx::mbar_init(&full[s], NF4 ? 1 + 16 : 1);
+      ptx::mbar_init(&full[s], MX4 ? 1 + 8 : (NF4 ? 1 + 16 : 1));
       ptx::mbar_init(&empty[s], 1);
       ptx::mbar_init(&cfull[s], 1);
     }
@@ -1399,7 +1399,55 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
   } else if (warp < 10) {
     // ----------------------------------------------------- NF4 decode warps
     // (bf16 B: the TMA brings the B tiles, these warps have nothing to do)
-    if constexpr (NF4) {
+    if constexpr (MX4) {
+      // Two groups of 4 warps take stages in turn; a thread decodes the 64
+      // codes (two blocks) of one row of B's stage, or of one k-row's half.
+      // Its wait for `empty` also tells this use of the stage's barriers from
+      // the one before (the other group's, whose codes it has not waited for).
+      const int group = (threadIdx.x - 64) >> 7, td = (threadIdx.x - 64) & 127;
+      const int r = B_MN ? td >> 1 : td, h = B_MN ? td & 1 : 0;
+      const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
+      const uint8_t* const cp = sC + (B_MN ? r * 64 + h * 32 : r * 32);
+      uint8_t* const dst = sB + h * 8192 + r * 128;
+      int gi = 0;
+      bool ok = true;
+      for (int j = 0; j < nitems && ok; ++j) {
+        const PairItem wi = pair_item(args, j, pair, npairs);
+        const PairTile tl = pair_tile(args, wi.t, mtiles, rank);
+        const int it_end = item_end(wi);
+        const int c0 = tl.n0 + (int)rank * 128;
+        // blocks of this thread's row that lie inside the matrix (TMA reads
+        // zeros beyond it, but a row can end inside its padded scales)
+        const int n = paired ? (rank == 0 ? tl.nb + r : args.pair_off + tl.nb + r) : c0 + r;
+        const int blocks = B_MN ? (args.N - c0 - h * 64) / 32 : (n < args.N ? args.K / 32 : 0);
+        const uint8_t* const sp = sS + r * 16 + (B_MN ? (c0 / 32 & 15) + h * 2 : 0);
+        for (int it = wi.kb0; it < it_end; ++it, ++gi) {
+          if ((gi ^ group) & 1) continue;
+          const int s = gi % STAGES;
+          const uint32_t ph = (gi / STAGES) & 1;
+          if (!ptx::mbar_wait_bounded(&empty[s], ph ^ 1, abort_flag) ||
+              !ptx::mbar_wait_bounded(&cfull[s], ph, abort_flag)) {
+            atomicOr(args.err, 1);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          if (it < num_kb) {
+            const uint4 w0 = *reinterpret_cast<const uint4*>(cp + s * C::C_STAGE);
+            const uint4 w1 = *reinterpret_cast<const uint4*>(cp + s * C::C_STAGE + 16);
+            const uint32_t sc = *reinterpret_cast<const uint16_t*>(sp + s * C::S_STAGE + (B_MN ? 0 : (it & 7) * 2));
+            const int left = B_MN ? blocks : blocks - it * 2;
+            const uint32_t ws0[4] = {w0.x, w0.y, w0.z, w0.w}, ws1[4] = {w1.x, w1.y, w1.z, w1.w};
+            uint8_t* const o = dst + s * C::B_STAGE;
+            decode_block_mx4(ws0, sc & 0xFF, left > 0, o, 0, r & 7);
+            decode_block_mx4(ws1, sc >> 8, left > 1, o, 4, r & 7);
+            ptx::fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(full0 + s * 8);
+        }
+      }
+    } else if constexpr (NF4) {
     const int td = threadIdx.x - 64;
     const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
     const uint32_t lane_b = C::LUT_LANES == 32 ? (uint32_t)lane * 8u : (uint32_t)(lane & 15) * 16u;
@@ -1412,7 +1460,7 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
       const int it_end = item_end(wi);
       int srow, unit0, chunk, coff, soff;
       bool valid;
-      if constexpr (!B_MN) {
+      if constexpr (BMD == B_NF4_K) {
         const int row = td >> 1, h = td & 1;
         const int n = paired ? (rank == 0 ? tl.nb + row : args.pair_off + tl.nb + row) : tl.n0 + (int)rank * 128 + row;
         valid = n < args.N;
@@ -1420,7 +1468,7 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
         unit0 = h * 4;
         chunk = 0;
         coff = row * 32 + h * 16;
-        soff = MX4 ? row * 16 + h : row * 4;
+        soff = row * 4;
       } else {
         const int q = td & 3, kr = td >> 2;
         const int col = tl.n0 + (int)rank * 128 + q * 32;
@@ -1429,16 +1477,15 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
         unit0 = (q & 1) * 4;
         chunk = q >> 1;
         coff = kr * 64 + q * 16;
-        soff = MX4 ? kr * 16 + ((tl.n0 + (int)rank * 128) / 32 & 15) + q
-                   : kr * 4 + ((tl.n0 + (int)rank * 128) / 64 & 3) + (q >> 1);
+        soff = kr * 4 + ((tl.n0 + (int)rank * 128) / 64 & 3) + (q >> 1);
       }
       uint8_t* const drow = sB + chunk * 8192 + srow * 128;
       for (int it = wi.kb0; it < it_end; ++it, ++gi) {
         const int s = gi % STAGES;
         const uint32_t ph = (gi / STAGES) & 1;
-        // cfull completes once per use of the slot (the tail stage arrives without bytes)
-        if (
-            !ptx::mbar_wait_bounded(&cfull[s], ph, abort_flag)) {
+        // cfull completes once per use of the slot (the tail stage arrives
+        // without bytes), after the producer has waited for `empty`
+        if (!ptx::mbar_wait_bounded(&cfull[s], ph, abort_flag)) {
           atomicOr(args.err, 1);
           *abort_flag = 1;
           ok = false;
@@ -1448,19 +1495,11 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
           const uint4 w = *reinterpret_cast<const uint4*>(sC + s * C::C_STAGE + coff);
           uint8_t* b = drow + s * C::B_STAGE;
           const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-          if constexpr (MX4) {
-            // one block of 32 per thread; K-major: the blocks of a last
-            // k-block that K ends inside are zeros (their scale bytes are padding)
-            const bool in_k = B_MN || it * BK + (unit0 >> 2) * 32 < args.K;
-            decode_block_mx4(ws, sS[s * C::S_STAGE + soff + (B_MN ? 0 : (it & 7) * 2)], valid && in_k, b, unit0,
-                             srow & 7);
-          } else {
-            const float am = reinterpret_cast<const float*>(sS + s * C::S_STAGE)[soff + (B_MN ? 0 : (it & 3))];
+          const float am = reinterpret_cast<const float*>(sS + s * C::S_STAGE)[soff + (B_MN ? 0 : (it & 3))];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint4 v = valid ? decode8_pairs<C::LUT_LANES>(ws[u], lutb, lane_b, am) : make_uint4(0, 0, 0, 0);
-              st_shared_v4(b + (((unit0 + u) ^ (srow & 7)) << 4), v);
-            }
+          for (int u = 0; u < 4; ++u) {
+            const uint4 v = valid ? decode8_pairs<C::LUT_LANES>(ws[u], lutb, lane_b, am) : make_uint4(0, 0, 0, 0);
+            st_shared_v4(b + (((unit0 + u) ^ (srow & 7)) << 4), v);
           }
           ptx::fence_proxy_async_smem();
         }
