@@ -60,6 +60,7 @@ using namespace soup;
 
 extern "C" size_t soup_linear_workspace(const soup_weight* W, int64_t T) {
   if (!W || T <= 0 || W->out_features <= 0 || W->in_features <= 0) return 0;
+  if (W->kind == SOUP_WEIGHT_MXFP4 && T <= MX4_MID_TOKENS) return 0;
   return std::max(workspace_bytes_for(T, W->out_features), workspace_bytes_for(T, W->in_features));
 }
 

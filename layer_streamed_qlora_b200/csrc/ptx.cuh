@@ -84,25 +84,6 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, limit_cycles));
 }
 
-// For loops whose pace the wait sets: 64 tries in place, the rest out of line
-// (the clock and flag handling in place made an issuing loop some 130 cycles
-// per k-block longer).  On expiry the slow part itself records `code` in the
-// error word and raises the flag.
-static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
-                                                   int code, long long limit_cycles) {
-  if (mbar_wait_bounded(bar, parity, abort_flag, limit_cycles)) return true;
-  atomicOr(err, code);
-  *abort_flag = 1;
-  return false;
-}
-__device__ __forceinline__ bool mbar_wait_fast(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
-                                               int code, long long limit_cycles = 4000000000LL) {
-#pragma unroll 1
-  for (int n = 0; n < 64; ++n)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, abort_flag, err, code, limit_cycles);
-}
-
 // ------------------------------------------------- CTA pairs (2-CTA clusters)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;

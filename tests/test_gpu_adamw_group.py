@@ -206,6 +206,37 @@ def test_8_bit_moments_follow_the_gradients():
     assert abs(m.mean() / 1e-3 - 1) < 0.07
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_tensors_aligned_to_16_bytes_only(bits):
+    """Views 16 but not 32 bytes into their storage give the bits of aligned tensors, and their neighbours stay."""
+    rng = np.random.default_rng(6)
+    n = 4100
+    a = make(n, bits, torch.float32, rng)
+    b, whole = {}, {}
+    for k, v in a.items():
+        skip = 16 // v.element_size() if "scale" not in k else 3
+        whole[k] = torch.full((n + 64,), 7, dtype=v.dtype, device="cuda")
+        b[k] = whole[k][skip:skip + v.numel()]
+        b[k].copy_(v)
+    for t in (a, b):
+        L.AdamWGroup([t], bits).step(**HP, t=5, seed=2, zero_grad=True)
+    for k, v in a.items():
+        skip = 16 // v.element_size() if "scale" not in k else 3
+        assert torch.equal(b[k].view(torch.uint8), v.view(torch.uint8)), k
+        assert (whole[k][:skip] == 7).all() and (whole[k][skip + v.numel():] == 7).all()
+
+
+def test_an_eps_near_zero_divides_by_the_root():
+    """eps below 1e-12 takes the IEEE path: a gradient of 1e-21 (its square subnormal in the second moment) still
+    moves theta by about the learning rate."""
+    n = 64
+    t = {k: torch.zeros(n, device="cuda") for k in ("theta", "m", "v")}
+    t["grad"] = torch.full((n,), 1e-21, device="cuda")
+    L.AdamWGroup([t], 32).step(1e-3, 0.0, 0.0, 1e-30, 0.0, 1.0, 1)
+    # v = 1e-42 is subnormal, with steps of 1.4e-45: its root is off by 1e-3 of itself
+    assert torch.allclose(t["theta"], torch.full((n,), -1e-3, device="cuda"), rtol=2e-3)
+
+
 def test_group_wrapper_refusals():
     t = make(64, 8, torch.float32, np.random.default_rng(4))
     with pytest.raises(ValueError, match="no tensors"):
