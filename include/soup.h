@@ -251,12 +251,13 @@ soup_status soup_lora_linear_bwd_noalloc(const soup_weight* W, const uint16_t* A
  *   soup_linear_bwd   dx [T, in] = dy [T, out] W     (W is frozen)
  * x, y, dy, dx bf16 with row strides (elements) of at least the row, each a
  * multiple of 8; fp32 accumulation, one rounding; out a multiple of 16, in of
- * 64 (MXFP4: of 32); pointers 16-byte aligned.  T = 0 is a no-op; outputs
- * beyond the row (between out and ldy) are left as they were.
+ * 64 (MXFP4: of 32); pointers 16-byte aligned; y and dx overlap no operand.
+ * T = 0 is a no-op; what lies between the rows of y and dx stays as it was.
  * workspace (optional, 256-byte aligned, soup_linear_workspace(W, T) bytes,
  * which can be 0; fewer or none is allowed and slower at some sizes): scratch
- * of this call alone: calls that may overlap on the GPU need one each.  Its contents need
- * no initialisation.  Asynchronous on `stream`; captures into graphs. */
+ * whose contents need no initialisation; calls that may overlap on the GPU,
+ * replayed graphs among them, need one each.  Asynchronous on `stream`;
+ * captures into graphs. */
 size_t soup_linear_workspace(const soup_weight* W, int64_t T);
 soup_status soup_linear_fwd(const soup_weight* W, const uint16_t* x, int64_t ldx, int64_t T, uint16_t* y, int64_t ldy,
                             void* workspace, size_t workspace_bytes, void* stream);

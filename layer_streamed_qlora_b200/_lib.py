@@ -401,6 +401,8 @@ def weight_bf16(w) -> SoupWeight:
 
 
 def weight_mxfp4(codes, scales, out_f, in_f) -> SoupWeight:
+    for name, t, n in (("codes", codes, out_f * in_f // 2), ("scales", scales, out_f * soup_mx4_scale_stride(in_f))):
+        _ptr("weight_mxfp4", name, t, t.get_device(), torch.uint8, n)
     return SoupWeight(SOUP_WEIGHT_MXFP4, out_f, in_f, codes.data_ptr(), None, None, scales.data_ptr())
 
 
@@ -460,12 +462,14 @@ class AdamWGroup:
                 setattr(a, k, p if n else None)
             if state_bits == 8:
                 for k in ("m_scale", "v_scale"):
-                    setattr(a, k, _ptr(fn, k, t[k], dev, torch.uint8, (n + 31) // 32) if n else None)
+                    setattr(a, k, _ptr(fn, k, t.get(k), dev, torch.uint8, (n + 31) // 32) if n else None)
         self._tensors = tensors
         self._handle = AdamWGroupHandle()
         nbytes = lib().soup_adamw_group_bytes(arr, len(tensors))
         self._dev = dev
-        self._tables = torch.empty(max(16, nbytes), dtype=torch.uint8, device="cuda")
+        # from the pool of the stream that fills it: what another stream freed may still be written there
+        with torch.cuda.stream(stream):
+            self._tables = torch.empty(max(16, nbytes), dtype=torch.uint8, device="cuda")
         _check(fn, lib().soup_adamw_group_init(arr, len(tensors), int(state_bits),
                                                SOUP_TYPE_F32 if grad is torch.float32 else SOUP_TYPE_BF16,
                                                _p(self._tables), self._tables.numel(), ctypes.byref(self._handle),

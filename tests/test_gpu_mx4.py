@@ -196,6 +196,21 @@ def test_products_with_no_tokens_and_non_finite_inputs():
     assert not nan.any()
 
 
+@pytest.mark.parametrize("T", [1, 13, 77, 1027])
+def test_products_leave_the_rows_behind_the_tokens(T):
+    """Rows beyond T are neither read (NaN there) nor written."""
+    W, Wb, keep = mx_weight(272, 96)
+    x = torch.full((T + 300, 96), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dy = torch.full((T + 300, 272), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x[:T], dy[:T] = torch.randn((T, 96), device="cuda"), torch.randn((T, 272), device="cuda")
+    y, dx = torch.full_like(dy, 7.0), torch.full_like(x, 7.0)
+    L.soup_linear_fwd(W, x[:T], y[:T])
+    L.soup_linear_bwd(W, dy[:T], dx[:T])
+    check_product(y[:T], x[:T], Wb.T, "y")
+    check_product(dx[:T], dy[:T], Wb, "dx")
+    assert (y[T:] == 7).all() and (dx[T:] == 7).all()
+
+
 @pytest.mark.parametrize("T,in_f", [(1, 4096), (40, 4096), (300, 4096), (1100, 8192)])
 def test_products_captured_replayed_and_concurrent(T, in_f):
     """Replays of one graph give the first run's bits, and two calls with a workspace each may overlap (1100 x 8192

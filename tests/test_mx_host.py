@@ -78,6 +78,16 @@ def test_linear_wrapper_refuses_host_tensors_and_shapes(L):
         L.soup_mx4_quantize(x.half(), None, None)
 
 
+def test_weight_refuses_short_or_wrong_buffers(L):
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8)
+    codes, scales = u8((64, 48)), u8((64, 16))
+    assert L.weight_mxfp4(codes, scales, 64, 96).scales == scales.data_ptr()
+    for c, s in ((codes[:63], scales), (codes, u8((64, 3))), (codes.int(), scales), (codes, scales.float()),
+                 (u8((64, 96))[:, :48], scales)):
+        with pytest.raises(ValueError, match="weight_mxfp4"):
+            L.weight_mxfp4(c, s, 64, 96)
+
+
 def test_layer_blob_holds_the_scales(L):
     cfg = L.LayerCfg(256, 2, 1, 128, 640, 16, 32.0, 1e-5, 5e5, 0, 0)
     w = L.soup_layer_blob_views(cfg, L.SOUP_WEIGHT_MXFP4, 0)
