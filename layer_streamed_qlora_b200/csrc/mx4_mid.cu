@@ -47,6 +47,9 @@ constexpr int GROUP_WARPS = 4;  // decode warps per k-block of a code load
 // of k-block i - CODE_KB before.  The wait's parity tells this phase from the
 // one before only if that one is over: i - CODE_KB - stages >= i - 2 stages.
 constexpr int MIN_A_STAGES = CODE_KB;
+// Tensor memory of the forward: the accumulator's columns, then MAX_STAGES
+// stages of A with 32 columns each.
+constexpr uint32_t A_COL = 256;
 constexpr int THREADS = 32 * (3 + GROUP_WARPS * CODE_KB);
 constexpr int CODE_BYTES = 16384, SCALE_BYTES = 2048, SCALE_BYTES_T = 4096;
 constexpr int BAR_BYTES = 512;
@@ -98,12 +101,13 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int b_bytes = a.bn * 128, a_stages = a.a_stages, x_stages = a.x_stages;
+  const int a_ring = TRANS ? a_stages * A_BYTES : 0;  // forward: in tensor memory
   uint8_t* sA = sm;
-  uint8_t* sB = sA + a_stages * A_BYTES;
+  uint8_t* sB = sA + a_ring;
   uint8_t* sC = sB + x_stages * b_bytes;
   uint8_t* sS = sC + CODE_SLOTS * CODE_BYTES;
   // the partial sums [bn][ROWS] fp32 take the stages' place when K is done
-  const int ring = a_stages * A_BYTES + x_stages * b_bytes + CODE_SLOTS * (CODE_BYTES + SCALE_BYTES_T), parts = a.bn * ROWS * 4;
+  const int ring = a_ring + x_stages * b_bytes + CODE_SLOTS * (CODE_BYTES + SCALE_BYTES_T), parts = a.bn * ROWS * 4;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + (ring > parts ? ring : parts));
   uint64_t* empty = full + MAX_STAGES;
   uint64_t* xfull = empty + MAX_STAGES;
@@ -123,7 +127,7 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
   const int kb0 = (int)((int64_t)slice * loads / a.slices) * CODE_KB;
   const int kb1 = min((int)((int64_t)(slice + 1) * loads / a.slices) * CODE_KB, num_kb);
   const int nk = kb1 - kb0;
-  const uint32_t cols = a.bn <= 32 ? 32 : (a.bn <= 64 ? 64 : (a.bn <= 128 ? 128 : 256));
+  const uint32_t cols = !TRANS ? 512 : (a.bn <= 32 ? 32 : (a.bn <= 64 ? 64 : (a.bn <= 128 ? 128 : 256)));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < MAX_STAGES; ++s) {
@@ -189,7 +193,8 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
       bool ok = true, ready = false;
       for (int i = 0; i < nk; ++i) {
         if (!ready && (!MID_WAIT_LANE(&xfull[xs], xph) || !MID_WAIT_LANE(&full[s], ph))) { ok = false; break; }
-        const uint32_t alo = a0 + s * (A_BYTES >> 4), blo = b0 + xs * (b_bytes >> 4);
+        const uint32_t alo = a0 + s * (A_BYTES >> 4), blo = b0 + xs * (b_bytes >> 4), ta = tmem + A_COL + s * 32;
+        ptx::tc_fence_after();
         uint64_t *const done = &empty[s], *const xdone = &xempty[xs];
         if (++s == a_stages) { s = 0; ph ^= 1; }
         if (++xs == x_stages) { xs = 0; xph ^= 1; }
@@ -197,9 +202,12 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
         // issued: a try takes 60 cycles to answer
         const bool r0 = ptx::mbar_try_wait(&xfull[xs], xph), r1 = ptx::mbar_try_wait(&full[s], ph);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          ptx::mma_bf16(tmem, ptx::desc_of(alo + k * A_STEP, HI), ptx::desc_of(blo + k * 2, HI), idesc,
-                        (i > 0 || k > 0) ? 1u : 0u);
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t bd = ptx::desc_of(blo + k * 2, HI);
+          const uint32_t acc = (i > 0 || k > 0) ? 1u : 0u;
+          if (TRANS) ptx::mma_bf16(tmem, ptx::desc_of(alo + k * A_STEP, HI), bd, idesc, acc);
+          else ptx::mma_bf16_ta(tmem, ta + k * 8, bd, idesc, acc);
+        }
         ptx::mma_commit(done);
         ptx::mma_commit(xdone);
         ready = r0 && r1;
@@ -209,7 +217,7 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
   } else {
     // forward: weight row t, its 64 codes of the group's k-block; backward:
     // k-row t / 2 of it, 64 of the 128 columns
-    const int group = (warp - 3) / GROUP_WARPS, t = (threadIdx.x - 96) & 127;
+    const int group = (warp - 3) / GROUP_WARPS, q = warp & 3, t = TRANS ? (threadIdx.x - 96) & 127 : q * 32 + lane;
     const int r = TRANS ? t >> 1 : t, h = TRANS ? t & 1 : 0;
     const uint32_t dst = ptx::smem_u32(TRANS ? sA + h * 8192 + r * 128 : sA + r * 128) ^ ((r & 7) << 4);
     // its two 16-byte units of codes (128-byte swizzled rows in the forward)
@@ -238,10 +246,17 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
       mx4_decode<4>(w, sc & 0xFF, v);
       mx4_decode<4>(w + 4, sc >> 8, v + 16);
       if (!free_now && !MID_WAIT(&empty[s], ph ^ 1)) break;
-      const uint32_t o = dst + s * A_BYTES;
+      if (TRANS) {
+        const uint32_t o = dst + s * A_BYTES;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) st_shared_v4(o ^ (u << 4), v + 4 * u);
-      ptx::fence_proxy_async_smem();
+        for (int u = 0; u < 8; ++u) st_shared_v4(o ^ (u << 4), v + 4 * u);
+        ptx::fence_proxy_async_smem();
+      } else {
+        ptx::tc_fence_after();
+        ptx::tmem_st32(tmem + ((uint32_t)(q * 32) << 16) + A_COL + s * 32, v);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+      }
       __syncwarp();
       if (lane == 0) {
         ptx::mbar_arrive(&full[s]);
@@ -255,7 +270,6 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
     // once every MMA has completed
     if (MID_WAIT(accf, 0)) {
       ptx::tc_fence_after();
-      const int q = warp & 3;
       float* part = reinterpret_cast<float*>(sm) + q * 32 + lane;
       for (int c = (warp - 3) >> 2; c < a.bn / 16; c += CODE_KB) {
         uint32_t v[16];
@@ -361,10 +375,13 @@ soup_status mx4_mid(const soup_weight* W, bool trans, const uint16_t* x, int64_t
   a.wait_limit = 4000000000LL;
   const int codes = CODE_SLOTS * (CODE_BYTES + SCALE_BYTES_T), room = 232448 - 1024 - BAR_BYTES - codes;
   const int xb = a.bn * 128;
-  a.x_stages = std::min(MAX_STAGES, (room - MIN_A_STAGES * A_BYTES) / xb);  // 3 at bn = 256
-  a.a_stages = std::min(MAX_STAGES, (room - a.x_stages * xb) / A_BYTES);
+  a.x_stages = std::min(MAX_STAGES, (room - (trans ? MIN_A_STAGES * A_BYTES : 0)) / xb);  // 3 (5) at bn = 256
+  a.a_stages = trans ? std::min(MAX_STAGES, (room - a.x_stages * xb) / A_BYTES) : MAX_STAGES;
   SOUP_CHECK(a.x_stages >= 2 && a.a_stages >= MIN_A_STAGES, SOUP_ERR_SHAPE, "frozen linear: %d tokens per tile", a.bn);
-  const size_t smem = 1024 + std::max(a.a_stages * A_BYTES + a.x_stages * xb + codes, a.bn * ROWS * 4) + BAR_BYTES;
+  // at least half of an SM's shared memory: a CTA that holds tensor memory and
+  // waits for its cluster must not share an SM with one that waits for the rest
+  const size_t smem = std::max<size_t>(
+      1024 + std::max((trans ? a.a_stages * A_BYTES : 0) + a.x_stages * xb + codes, a.bn * ROWS * 4) + BAR_BYTES, 120 << 10);
   CUtensorMap map[3];
   const int64_t out = W->out_features, in = W->in_features;
   SOUP_TRY(make_map(&map[0], x, CU_BF16, a.K, T, ldx * 2, 64, (uint32_t)a.bn, CU_SWIZZLE_128, "x"));
