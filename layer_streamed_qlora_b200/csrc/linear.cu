@@ -11,7 +11,7 @@
 // against the engine at 6144 x 4096 (us):
 //   T           1     16    33    256   512   1024   2048
 //   mx4_few     8.0   11.9  19.9 (T = 32)
-//   mx4_mid     14.8  16    16.8  22.4  32.6  62
+//   mx4_mid     14.8  15    15.4  20.6  28.8  54
 //   engine      37    37    37    36.5  54.7  65     113
 // so mx4_few takes up to 16 tokens of the forward, mx4_mid up to 1024.
 #include <algorithm>

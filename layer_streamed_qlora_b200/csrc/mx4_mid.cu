@@ -14,14 +14,20 @@
 //
 // Warps: 0 TMA of the x tiles, 1 MMA, 2 TMA of codes and scales, 3..18 decode:
 // four groups of 4, one for each of the four k-blocks of a code load; a thread
-// turns two blocks of 32 codes into bf16 and stores them in the swizzled A
-// stage (two, to share the waits, fences and addresses).
+// turns two blocks of 32 codes into bf16 (two, to share the waits, fences and
+// addresses).  In the forward a thread's 64 values are one row of A, and go to
+// tensor memory as the A operand: neither the stores nor the MMA's reads of A
+// take shared memory's port then (256 tokens through 28672 x 4096: 65 -> 57
+// us).  In the backward they are parts of 64 rows, and go to the swizzled
+// stage in shared memory.
 //
-// What bounds it: per k-block the decode takes about 330 cycles of the integer
-// pipes and the issuing lane some 350 (two barrier tries of 60 cycles, four
-// MMAs, two commits), the tensor core 2 cycles per token.  256 tokens through
-// 28672 x 4096 take 65 us (924 TFLOP/s), 64 take 49 us; the GEMM engine's
-// 256-token tiles take 84 us for either.
+// What bounds it (forward, one CTA per SM, cycles per k-block from the slope
+// over K): 490 with up to 64 tokens, 620 with 176, 730 with 256.  With the
+// decode left out 300 remain of the 490, and all of the 730: there the x tile
+// is the limit, 32 KB per k-block and SM from L2 (45 bytes a clock), and the
+// tensor core needs 512.  Weights in L2 instead of HBM make no difference.
+// 256 tokens through 28672 x 4096 take 57 us (1060 TFLOP/s), 64 take 45 us;
+// the GEMM engine's 256-token tiles take 84 us for either.
 
 #include <cuda.h>
 
@@ -38,11 +44,17 @@ namespace {
 constexpr int ROWS = 128;             // weight rows (columns) per CTA
 constexpr int A_BYTES = ROWS * 128;   // one 64-wide k-block of A
 constexpr int MAX_STAGES = 8;  // of the A ring and of the x ring
-// Codes come CODE_KB k-blocks at a time: 128 rows x 128 bytes (swizzled) and
-// 16 scale bytes per row (of 8 k-blocks, two loads' worth), or 256 k-rows x
-// 64 bytes and 16 scale bytes per k-row.
-constexpr int CODE_KB = 4, CODE_SLOTS = 3;
-constexpr int GROUP_WARPS = 4;  // decode warps per k-block of a code load
+// Decode groups, and warps of one.
+constexpr int GROUPS = 4, GROUP_WARPS = 4;
+// Codes come CODE_KB k-blocks at a time, one for each group: 128 rows x 128
+// bytes (swizzled) and 16 scale bytes per row (of 8 k-blocks, two loads'
+// worth), or 256 k-rows x 64 bytes and 16 scale bytes per k-row.
+constexpr int CODE_KB = GROUPS, CODE_SLOTS = 3;
+template <bool TRANS>
+struct Codes {
+  static constexpr int BYTES = 16384, SCALE_BYTES = TRANS ? 4096 : 2048;
+  static constexpr int ALL = CODE_SLOTS * (BYTES + SCALE_BYTES);
+};
 // A decode group that waits for the stage of k-block i has waited for the one
 // of k-block i - CODE_KB before.  The wait's parity tells this phase from the
 // one before only if that one is over: i - CODE_KB - stages >= i - 2 stages.
@@ -50,8 +62,7 @@ constexpr int MIN_A_STAGES = CODE_KB;
 // Tensor memory of the forward: the accumulator's columns, then MAX_STAGES
 // stages of A with 32 columns each.
 constexpr uint32_t A_COL = 256;
-constexpr int THREADS = 32 * (3 + GROUP_WARPS * CODE_KB);
-constexpr int CODE_BYTES = 16384, SCALE_BYTES = 2048, SCALE_BYTES_T = 4096;
+constexpr int THREADS = 32 * (3 + GROUP_WARPS * GROUPS);
 constexpr int BAR_BYTES = 512;
 
 struct MidArgs {
@@ -89,6 +100,18 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t* v) {
                : "memory");
 }
 
+// Two blocks of 32 codes with the two bytes of scales, of which the first
+// `left` are in the matrix and the others are zeros.
+__device__ __forceinline__ void decode_64(uint32_t* w, uint32_t sc, int left, uint32_t* v) {
+  if (left < 2) {
+    w[4] = w[5] = w[6] = w[7] = 0;
+    sc &= 0xFF;
+    if (left < 1) w[0] = w[1] = w[2] = w[3] = sc = 0;
+  }
+  mx4_decode<4>(w, sc & 0xFF, v);
+  mx4_decode<4>(w + 4, sc >> 8, v + 16);
+}
+
 // By one lane of a warp, and by all lanes with one answer.
 #define MID_FAILED (atomicOr(a.err, 1), *abort_flag = 1, false)
 #define MID_WAIT_LANE(bar, parity) (ptx::mbar_wait_bounded((bar), (parity), abort_flag, a.wait_limit) || MID_FAILED)
@@ -98,6 +121,7 @@ template <bool TRANS>
 __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant__ CUtensorMap tmx,
                                                           const __grid_constant__ CUtensorMap tmc,
                                                           const __grid_constant__ CUtensorMap tms, const MidArgs a) {
+  using CO = Codes<TRANS>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int b_bytes = a.bn * 128, a_stages = a.a_stages, x_stages = a.x_stages;
@@ -105,9 +129,9 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
   uint8_t* sA = sm;
   uint8_t* sB = sA + a_ring;
   uint8_t* sC = sB + x_stages * b_bytes;
-  uint8_t* sS = sC + CODE_SLOTS * CODE_BYTES;
+  uint8_t* sS = sC + CODE_SLOTS * CO::BYTES;
   // the partial sums [bn][ROWS] fp32 take the stages' place when K is done
-  const int ring = a_ring + x_stages * b_bytes + CODE_SLOTS * (CODE_BYTES + SCALE_BYTES_T), parts = a.bn * ROWS * 4;
+  const int ring = a_ring + x_stages * b_bytes + CO::ALL, parts = a.bn * ROWS * 4;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + (ring > parts ? ring : parts));
   uint64_t* empty = full + MAX_STAGES;
   uint64_t* xfull = empty + MAX_STAGES;
@@ -138,7 +162,7 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
     }
     for (int g = 0; g < CODE_SLOTS; ++g) {
       ptx::mbar_init(&cfull[g], 1);
-      ptx::mbar_init(&cempty[g], GROUP_WARPS * CODE_KB);
+      ptx::mbar_init(&cempty[g], GROUP_WARPS * GROUPS);
     }
     ptx::mbar_init(accf, 1);
     *abort_flag = 0;
@@ -173,9 +197,9 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
       uint32_t gph = 0;
       for (int kb = kb0; kb < kb1; kb += CODE_KB) {
         if (!MID_WAIT_LANE(&cempty[g], gph ^ 1)) break;
-        ptx::mbar_arrive_expect_tx(&cfull[g], CODE_BYTES + (TRANS ? SCALE_BYTES_T : SCALE_BYTES));
-        ptx::tma_load_2d(sC + g * CODE_BYTES, &tmc, &cfull[g], TRANS ? m0 / 2 : kb * 32, TRANS ? kb * 64 : m0);
-        ptx::tma_load_2d(sS + g * SCALE_BYTES_T, &tms, &cfull[g], (TRANS ? m0 / 32 : kb * 2) & ~15,
+        ptx::mbar_arrive_expect_tx(&cfull[g], CO::BYTES + CO::SCALE_BYTES);
+        ptx::tma_load_2d(sC + g * CO::BYTES, &tmc, &cfull[g], TRANS ? m0 / 2 : kb * 32, TRANS ? kb * 64 : m0);
+        ptx::tma_load_2d(sS + g * CO::SCALE_BYTES, &tms, &cfull[g], (TRANS ? m0 / 32 : kb * 2) & ~15,
                          TRANS ? kb * 64 : m0);
         if (++g == CODE_SLOTS) { g = 0; gph ^= 1; }
       }
@@ -219,7 +243,6 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
     // k-row t / 2 of it, 64 of the 128 columns
     const int group = (warp - 3) / GROUP_WARPS, q = warp & 3, t = TRANS ? (threadIdx.x - 96) & 127 : q * 32 + lane;
     const int r = TRANS ? t >> 1 : t, h = TRANS ? t & 1 : 0;
-    const uint32_t dst = ptx::smem_u32(TRANS ? sA + h * 8192 + r * 128 : sA + r * 128) ^ ((r & 7) << 4);
     // its two 16-byte units of codes (128-byte swizzled rows in the forward)
     const uint32_t c0 = ptx::smem_u32(sC) + (TRANS ? group * 4096 + r * 64 + h * 32 : r * 128 + (((group * 2) ^ (r & 7)) << 4));
     const uint32_t c1 = c0 ^ 16;
@@ -228,23 +251,19 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
     // TMA reads zeros beyond the matrix, but a row can end inside its padded
     // scales: blocks from `blocks` on are none
     const int blocks = TRANS ? (a.M - m0 - h * 64 + 31) / 32 : (m0 + r < a.M ? a.K / 32 : 0);
+    // where its 64 values go: tensor memory, or a row of the swizzled stage
+    const uint32_t dst = TRANS ? ptx::smem_u32(sA + h * 8192 + r * 128) ^ ((r & 7) << 4)
+                               : tmem + ((uint32_t)(q * 32) << 16) + A_COL;
     int s = group, g = 0;
     uint32_t ph = 0, gph = 0;
     for (int kb = kb0; kb + group < kb1; kb += CODE_KB) {
       if (!MID_WAIT(&cfull[g], gph)) break;
       uint32_t w[8], v[32];
-      ld_shared_v4(c0 + g * CODE_BYTES, w);
-      ld_shared_v4(c1 + g * CODE_BYTES, w + 4);
-      uint32_t sc = ld_shared_u16(s0 + g * SCALE_BYTES_T + (TRANS ? 0 : (kb & 4) * 2));
-      const int left = TRANS ? blocks : blocks - (kb + group) * 2;
-      if (left < 2) {
-        w[4] = w[5] = w[6] = w[7] = 0;
-        sc &= 0xFF;
-        if (left < 1) w[0] = w[1] = w[2] = w[3] = sc = 0;
-      }
+      ld_shared_v4(c0 + g * CO::BYTES, w);
+      ld_shared_v4(c1 + g * CO::BYTES, w + 4);
+      const uint32_t sc = ld_shared_u16(s0 + g * CO::SCALE_BYTES + (TRANS ? 0 : (kb & 4) * 2));
       const bool free_now = __all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(&empty[s], ph ^ 1));
-      mx4_decode<4>(w, sc & 0xFF, v);
-      mx4_decode<4>(w + 4, sc >> 8, v + 16);
+      decode_64(w, sc, TRANS ? blocks : blocks - (kb + group) * 2, v);
       if (!free_now && !MID_WAIT(&empty[s], ph ^ 1)) break;
       if (TRANS) {
         const uint32_t o = dst + s * A_BYTES;
@@ -253,7 +272,7 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
         ptx::fence_proxy_async_smem();
       } else {
         ptx::tc_fence_after();
-        ptx::tmem_st32(tmem + ((uint32_t)(q * 32) << 16) + A_COL + s * 32, v);
+        ptx::tmem_st32(dst + s * 32, v);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
       }
@@ -263,7 +282,7 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
         ptx::mbar_arrive(&cempty[g]);
       }
       if (++g == CODE_SLOTS) { g = 0; gph ^= 1; }
-      s += CODE_KB;
+      s += GROUPS;
       if (s >= a_stages) { s -= a_stages; ph ^= 1; }
     }
     // the accumulator to shared memory as [token][row]: the stages are free
@@ -271,7 +290,7 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
     if (MID_WAIT(accf, 0)) {
       ptx::tc_fence_after();
       float* part = reinterpret_cast<float*>(sm) + q * 32 + lane;
-      for (int c = (warp - 3) >> 2; c < a.bn / 16; c += CODE_KB) {
+      for (int c = (warp - 3) >> 2; c < a.bn / 16; c += GROUPS) {
         uint32_t v[16];
         ptx::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c * 16, v);
         ptx::tmem_ld_wait();
@@ -369,11 +388,11 @@ soup_status mx4_mid(const soup_weight* W, bool trans, const uint16_t* x, int64_t
   // up to 4 slices: clusters of 8 one-per-SM CTAs do not find room at once
   // (64 tokens through 2048 x 11008: 30 us with 8 slices, 21.5 with 4, 33 with 2)
   a.slices = 1;
-  while (a.slices < 4 && rtiles * ttiles * a.slices * 2 <= sm_count() && num_kb / (a.slices * 2) >= CODE_KB) a.slices *= 2;
+  while (a.slices < 4 && rtiles * ttiles * a.slices * 2 <= sm_count() && num_kb / (a.slices * 2) >= GROUPS) a.slices *= 2;
   a.err = device_error_word();
   SOUP_CHECK(a.err != nullptr, SOUP_ERR_CUDA, "device error word unavailable");
   a.wait_limit = 4000000000LL;
-  const int codes = CODE_SLOTS * (CODE_BYTES + SCALE_BYTES_T), room = 232448 - 1024 - BAR_BYTES - codes;
+  const int codes = trans ? Codes<true>::ALL : Codes<false>::ALL, room = 232448 - 1024 - BAR_BYTES - codes;
   const int xb = a.bn * 128;
   a.x_stages = std::min(MAX_STAGES, (room - (trans ? MIN_A_STAGES * A_BYTES : 0)) / xb);  // 3 (5) at bn = 256
   a.a_stages = trans ? std::min(MAX_STAGES, (room - a.x_stages * xb) / A_BYTES) : MAX_STAGES;
