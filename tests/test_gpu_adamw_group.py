@@ -265,3 +265,27 @@ def test_group_made_and_stepped_on_a_side_stream():
     torch.cuda.synchronize()
     for k in a:
         assert torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)), k
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_elements_beyond_32_bits(bits):
+    """The last elements of a tensor of more than 2^31 step as they do in a tensor of their own (8-bit codes are
+    rounded by other random bits: within one)."""
+    n, tail = 2 ** 31 + 5000, 4096 + 904  # the tail starts on a block of 32
+    state = torch.uint8 if bits == 8 else torch.float32
+    big = {"theta": torch.zeros(n, device="cuda"), "grad": torch.zeros(n, dtype=torch.bfloat16, device="cuda"),
+           "m": torch.zeros(n, dtype=state, device="cuda"), "v": torch.zeros(n, dtype=state, device="cuda")}
+    if bits == 8:
+        big |= {k: torch.zeros((n + 31) // 32, dtype=torch.uint8, device="cuda") for k in ("m_scale", "v_scale")}
+    small = make(tail, bits, torch.bfloat16, np.random.default_rng(11), bf16=False)
+    for k, v in big.items():
+        v[-small[k].numel():] = small[k]
+    for t in (big, small):
+        L.AdamWGroup([t], bits).step(**HP, t=7, seed=3)
+    for k, v in big.items():
+        a, b = v[-small[k].numel():], small[k]
+        if bits == 8 and k in ("m", "v"):
+            assert (a.int() - b.int()).abs().max() <= 1, k
+        else:
+            assert torch.equal(a, b), k
+    assert not big["theta"][:2 ** 31 - 8].any()

@@ -92,6 +92,56 @@ def test_dequantise_every_code_and_scale():
     assert np.array_equal(Wb.double().cpu().numpy(), want, equal_nan=True)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_buffers_aligned_to_16_bytes_only(dtype):
+    """W, codes, scales and the stored values 16 but not 32 bytes into their storage, rows too: the aligned bits."""
+    out_f, in_f, e = 37, 544, 16 // dtype.itemsize
+    whole = torch.randn((out_f, in_f + e), device="cuda").to(dtype)
+    W = whole[:, e:]                  # row stride 16 bytes beyond a multiple of 32
+    assert W.data_ptr() % 32 == 16
+    ss_ = mx.scale_stride(in_f)
+    flat = lambda n, t, skip: torch.full((n + 64,), 7, dtype=t, device="cuda")[skip:skip + n]
+    codes, scales = flat(out_f * in_f // 2, torch.uint8, 16), flat(out_f * ss_, torch.uint8, 16)
+    Wb, Wd = flat(out_f * in_f, torch.bfloat16, 8), flat(out_f * in_f, torch.bfloat16, 8)
+    L.soup_mx4_quantize(W, codes, scales, Wb)
+    L.soup_mx4_dequant(codes, scales, out_f, in_f, Wd)
+    c0, s0, W0 = quantize(W.contiguous(), values=True)
+    assert torch.equal(codes.view_as(c0), c0) and torch.equal(scales.view_as(s0), s0)
+    assert torch.equal(Wb.view_as(W0), W0) and torch.equal(Wd, Wb)
+    x = torch.randn((40, in_f), device="cuda").to(torch.bfloat16)
+    for T in (3, 40):
+        y = torch.empty((T, out_f // 16 * 16), dtype=torch.bfloat16, device="cuda")
+        L.soup_linear_fwd(L.weight_mxfp4(codes, scales, out_f // 16 * 16, in_f), x[:T], y)
+        check_product(y, x[:T], W0[:out_f // 16 * 16].T, "y")
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^32 weights: the last rows quantise, dequantise and multiply as they do on their own."""
+    out_f, in_f, n = 131_200, 32_768, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    W = torch.empty((out_f, in_f), dtype=torch.bfloat16, device="cuda")
+    for r in range(0, out_f, 8200):
+        W[r:r + 8200] = torch.randn((8200, in_f), generator=g, device="cuda") * 0.02
+    codes, scales, _ = quantize(W)
+    c0, s0, last = quantize(W[-n:].contiguous(), values=True)
+    assert torch.equal(codes[-n:], c0) and torch.equal(scales[-n:], s0)
+    L.soup_mx4_dequant(codes, scales, out_f, in_f, W)
+    assert torch.equal(W[-n:], last)
+    del W
+    w = L.weight_mxfp4(codes, scales, out_f, in_f)
+    for T in (1, 40, 1100):
+        ws = torch.empty(L.soup_linear_workspace(w, T), dtype=torch.uint8, device="cuda")
+        x = torch.randn((T, in_f), generator=g, device="cuda").to(torch.bfloat16)
+        y = torch.empty((T, out_f), dtype=torch.bfloat16, device="cuda")
+        L.soup_linear_fwd(w, x, y, workspace=ws)
+        check_product(y[:, -n:], x, last.T, f"y, T={T}")
+        dy = torch.zeros((T, out_f), dtype=torch.bfloat16, device="cuda")
+        dy[:, -n:] = torch.randn((T, n), generator=g, device="cuda")
+        dx = torch.empty((T, in_f), dtype=torch.bfloat16, device="cuda")
+        L.soup_linear_bwd(w, dy, dx, workspace=ws)
+        check_product(dx, dy[:, -n:], last, f"dx, T={T}")
+
+
 def mx_weight(out_f, in_f, seed=5, std=0.02):
     W = torch.from_numpy(ss.normal_f32(seed, f"w{out_f}x{in_f}", (out_f, in_f), std=std)).cuda()
     codes, scales, Wb = quantize(W, values=True)
@@ -194,6 +244,25 @@ def test_products_with_no_tokens_and_non_finite_inputs():
     assert nan[1].all() and nan[:, 7].all()
     nan[1], nan[:, 7] = False, False
     assert not nan.any()
+
+
+@pytest.mark.parametrize("kind", ["mxfp4", "bf16"])
+def test_products_with_less_workspace(kind):
+    """Any size of workspace is allowed; what lies behind it stays."""
+    W, Wb, keep = mx_weight(2064, 8224)
+    if kind == "bf16":
+        Wb = Wb[:, :8192].contiguous()  # a weight holds pointers, not tensors
+        W = L.weight_bf16(Wb)
+    in_f = Wb.shape[1]
+    x = torch.randn((1100, in_f), device="cuda").to(torch.bfloat16)
+    full = L.soup_linear_workspace(W, 1100)
+    assert full > 4 << 20
+    for n in (1, 3000, 600_000, 1 << 20, full // 2 + 17, full):
+        buf = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        y = torch.empty((1100, 2064), dtype=torch.bfloat16, device="cuda")
+        L.soup_linear_fwd(W, x, y, workspace=buf[:n])
+        check_product(y, x, Wb.T, f"{n} bytes")
+        assert (buf[n:] == 0x5A).all()
 
 
 @pytest.mark.parametrize("T", [1, 13, 77, 1027])
