@@ -20,6 +20,11 @@ def test_scale_stride(L):
     assert [L.soup_mx4_scale_stride(i) for i in (32, 512, 544, 4096)] == [16, 16, 32, 128]
 
 
+def test_scale_stride_is_the_librarys(L):
+    f = L.lib().soup_mx4_scale_stride
+    assert all(L.soup_mx4_scale_stride(i) == f(i) for i in (-32, 0, 1, 31, 32, 512, 513, 544, 4096, 14336, 1 << 29))
+
+
 def test_quantise_refusals(L):
     f = L.lib().soup_mx4_quantize
 
