@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const void* __restric
                                                            int64_t scale_stride, uint8_t* __restrict__ values,
                                                            bool v32_in, bool v32_out, bool dense, bool packed,
                                                            int32_t* __restrict__ nonfinite) {
+  ptx::grid_dep_wait();
   const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const bool in_range = u < units;  // the same for both halves of a block
   uint32_t row = 0, c = 0;
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(256) mx4_dequant_kernel(const uint2* __restric
                                                           const uint8_t* __restrict__ scales, int64_t units,
                                                           uint32_t units_per_row, int64_t scale_stride,
                                                           uint8_t* __restrict__ out, bool v32, bool dense) {
+  ptx::grid_dep_wait();
   const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (u >= units) return;
   const uint2 c = __ldg(codes + u);
@@ -166,12 +168,11 @@ extern "C" soup_status soup_mx4_quantize(const void* W, int32_t w_type, int64_t 
   const bool dense = ss == in / 32, packed = ldw == in || out == 1;
   uint2* c = reinterpret_cast<uint2*>(codes);
   uint8_t* v = reinterpret_cast<uint8_t*>(W_bf16);
-  if (w_type == SOUP_TYPE_BF16)
-    mx4_quantize_kernel<true><<<grid, 256, 0, st>>>(W, units, upr, ldw, c, scales, ss, v, v32_in, v32_out, dense,
-                                                    packed, nonfinite_dev);
-  else
-    mx4_quantize_kernel<false><<<grid, 256, 0, st>>>(W, units, upr, ldw, c, scales, ss, v, v32_in, v32_out, dense,
-                                                     packed, nonfinite_dev);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = dependent_launch(grid, 256, 0, st, attr);
+  SOUP_CUDA_TRY(cudaLaunchKernelEx(&cfg, w_type == SOUP_TYPE_BF16 ? mx4_quantize_kernel<true> : mx4_quantize_kernel<false>,
+                                   W, units, upr, ldw, c, scales, ss, v, v32_in, v32_out, dense, packed,
+                                   nonfinite_dev));
   SOUP_LAUNCH_CHECK();
   return SOUP_OK;
 }
@@ -183,9 +184,12 @@ extern "C" soup_status soup_mx4_dequant(const uint8_t* codes, const uint8_t* sca
   SOUP_CHECK(soup_aligned(codes, 16) && soup_aligned(scales, 16) && soup_aligned(W_bf16, 16), SOUP_ERR_ALIGN,
              "soup_mx4_dequant: codes, scales and W_bf16 must be 16-byte aligned");
   const int64_t units = out * (in / 16), ss = mx4_scale_stride(in);
-  mx4_dequant_kernel<<<(unsigned)((units + 255) / 256), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-      reinterpret_cast<const uint2*>(codes), scales, units, (uint32_t)(in / 16), ss,
-      reinterpret_cast<uint8_t*>(W_bf16), soup_aligned(W_bf16, 32), ss == in / 32);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      dependent_launch((unsigned)((units + 255) / 256), 256, 0, static_cast<cudaStream_t>(stream), attr);
+  SOUP_CUDA_TRY(cudaLaunchKernelEx(&cfg, mx4_dequant_kernel, reinterpret_cast<const uint2*>(codes), scales, units,
+                                   (uint32_t)(in / 16), ss, reinterpret_cast<uint8_t*>(W_bf16),
+                                   (bool)soup_aligned(W_bf16, 32), ss == in / 32));
   SOUP_LAUNCH_CHECK();
   return SOUP_OK;
 }

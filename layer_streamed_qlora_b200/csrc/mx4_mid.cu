@@ -178,6 +178,8 @@ __global__ void __launch_bounds__(THREADS) mx4_mid_kernel(const __grid_constant_
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
 
   if (warp == 0) {
@@ -353,19 +355,13 @@ template <bool TRANS>
 soup_status launch_mid(const CUtensorMap (&map)[3], const MidArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
   auto kern = mx4_mid_kernel<TRANS>;
   SOUP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448));
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)a.slices;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = dependent_launch(grid, THREADS, smem, st, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.slices;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
   SOUP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, map[0], map[1], map[2], a));
   SOUP_LAUNCH_CHECK();
   return SOUP_OK;

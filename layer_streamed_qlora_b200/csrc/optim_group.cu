@@ -204,6 +204,7 @@ __device__ __forceinline__ uint32_t block_top(const float (&x)[8], bool& odd) {
 // tensor's end (in its last chunk alone) count as zeros and are not stored.
 template <int BITS, bool G16>
 __global__ void __launch_bounds__(256, 4) adamw_group_kernel(const GroupArgs a) {
+  ptx::grid_dep_wait();
   bool bad = false;
   for (int64_t c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
     const GroupChunk ch = a.chunks[c];
@@ -527,13 +528,11 @@ extern "C" soup_status soup_adamw_group_step(const soup_adamw_group* group, floa
   const double gb = g16 ? 2 : 4;
   profile_begin(st, GC_ADAMW, 0.0,
                 (double)group->n_elements * (10.0 + gb * (zero_grad ? 2 : 1) + (group->state_bits == 32 ? 16.0 : 4.125)));
-  if (group->state_bits == 32) {
-    if (g16) adamw_group_kernel<32, true><<<grid, 256, 0, st>>>(a);
-    else adamw_group_kernel<32, false><<<grid, 256, 0, st>>>(a);
-  } else {
-    if (g16) adamw_group_kernel<8, true><<<grid, 256, 0, st>>>(a);
-    else adamw_group_kernel<8, false><<<grid, 256, 0, st>>>(a);
-  }
+  auto* kern = group->state_bits == 32 ? (g16 ? adamw_group_kernel<32, true> : adamw_group_kernel<32, false>)
+                                       : (g16 ? adamw_group_kernel<8, true> : adamw_group_kernel<8, false>);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = dependent_launch(grid, 256, 0, st, attr);
+  SOUP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, a));
   SOUP_LAUNCH_CHECK();
   profile_end(st);
   return SOUP_OK;

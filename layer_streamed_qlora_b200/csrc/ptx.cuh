@@ -84,6 +84,14 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, limit_cycles));
 }
 
+// Programmatic dependent launch: a kernel launched with the attribute may
+// start once every CTA of the one before it has ended or called
+// grid_dep_launch (after its own grid_dep_wait, so that no third kernel
+// starts); its grid_dep_wait returns when that one has completed and its
+// writes are seen.
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------- CTA pairs (2-CTA clusters)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;

@@ -5,6 +5,7 @@
 
 #include <cstdint>
 #include <cstdio>
+#include <cstring>
 #include <cuda_runtime.h>
 
 #include "../../include/soup.h"
@@ -61,6 +62,25 @@ enum GemmClass : int {
 bool profiling();
 void profile_begin(cudaStream_t st, int cls, double flops, double bytes);
 void profile_end(cudaStream_t st);
+
+// Configuration of a launch that may start while the stream's last kernel
+// ends: its kernel calls ptx::grid_dep_wait before it touches memory, which
+// returns when that one has completed.  Set-up and launch latency are hidden
+// behind it (one attribute at attr[0]).
+inline cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, size_t smem, cudaStream_t st,
+                                           cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
 
 }  // namespace soup
 

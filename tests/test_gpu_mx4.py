@@ -311,6 +311,62 @@ def test_products_captured_replayed_and_concurrent(T, in_f):
     assert all(torch.equal(y, w) for y, w in zip(ys, want))
 
 
+@pytest.mark.parametrize("T", [1, 50])
+def test_a_chain_of_launches_sees_what_came_before(T):
+    """Each launch may start while the one before it ends: a chain in which every call reads what the last one
+    wrote, and one overwrites what the last one read, gives the bits of the calls made one by one; eagerly, and
+    captured with a fork and a join."""
+    n = 1024
+    W0 = torch.randn((n, n), device="cuda") * 0.03
+    new = lambda: dict(codes=torch.zeros((n, n // 2), dtype=torch.uint8, device="cuda"),
+                       scales=torch.zeros((n, n // 32), dtype=torch.uint8, device="cuda"),
+                       Wb=torch.zeros((n, n), dtype=torch.bfloat16, device="cuda"),
+                       x=torch.ones((T, n), dtype=torch.bfloat16, device="cuda"),
+                       y=torch.zeros((T, n), dtype=torch.bfloat16, device="cuda"),
+                       z=torch.zeros((T, n), dtype=torch.bfloat16, device="cuda"))
+
+    def chain(b, between):
+        w = L.weight_mxfp4(b["codes"], b["scales"], n, n)
+        side = torch.cuda.Stream()
+        L.soup_mx4_quantize(W0, b["codes"], b["scales"])
+        for _ in range(4):
+            between()
+            L.soup_linear_fwd(w, b["x"], b["y"])
+            between()
+            side.wait_stream(torch.cuda.current_stream())
+            L.soup_linear_bwd(w, b["y"], b["z"], stream=side)       # reads y
+            L.soup_mx4_dequant(b["codes"], b["scales"], n, n, b["Wb"])
+            torch.cuda.current_stream().wait_stream(side)
+            between()
+            L.soup_linear_fwd(w, b["z"], b["x"])                    # overwrites the first product's input
+            between()
+            L.soup_mx4_quantize(b["Wb"], b["codes"], b["scales"])   # overwrites the weight just read
+            between()
+            L.soup_mx4_dequant(b["codes"], b["scales"], n, n, b["Wb"])
+
+    want = new()
+    chain(want, torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    got = new()
+    torch.cuda.synchronize()
+    chain(got, lambda: None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    assert torch.isfinite(got["x"]).all() and got["x"].any()
+    cap = new()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain(cap, lambda: None)
+    for _ in range(3):
+        cap["x"].fill_(1)
+        for k in ("codes", "scales", "Wb"):
+            cap[k].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(cap[k], want[k]) for k in want)
+
+
 @pytest.mark.parametrize("T,in_f", [(64, 512), (1, 512), (300, 544)])
 def test_lora_linear_over_mxfp4(T, in_f):
     out_f, r, s = 512, 8, 2.0
