@@ -9,11 +9,15 @@
 // slices and 11.8 whole), summed in slice order.
 // MXFP4 weights with fewer tokens have kernels of their own, both measured
 // against the engine at 6144 x 4096 (us):
-//   T           1     16    33    256   512   1024   2048
-//   mx4_few     8.0   11.9  19.9 (T = 32)
-//   mx4_mid     14.8  15    15.4  20.6  28.8  54
-//   engine      37    37    37    36.5  54.7  65     113
-// so mx4_few takes up to 16 tokens of the forward, mx4_mid up to 1024.
+//   T           1     8     16    33    256   512   1024   2048
+//   mx4_few     7.8   8.2   16.1  19.9 (T = 32)
+//   mx4_mid     13.8  14    14.1  14.5  19.5  28.2  53
+//   engine      37    37    37    37    36.5  54.7  65     89
+// so mx4_few takes up to 8 tokens of the forward and mx4_mid up to 1024.  From
+// 9 to 16 tokens mx4_few needs twice the registers and instructions, and wins
+// only where each SM has one of its CTAs at most (16 rows each): 14.1 us
+// against 16.9 at 2048 x 11008, but 23 against 22 at 4096 x 14336 and 52
+// against 42 at 28672 x 4096.
 #include <algorithm>
 
 #include "gemm.h"
@@ -69,7 +73,8 @@ extern "C" soup_status soup_linear_fwd(const soup_weight* W, const uint16_t* x, 
   SOUP_TRY(check_linear("soup_linear_fwd", W, x, ldx, W ? W->in_features : 0, T, y, ldy, W ? W->out_features : 0,
                         workspace, workspace_bytes));
   if (T == 0) return SOUP_OK;
-  if (W->kind == SOUP_WEIGHT_MXFP4 && T <= MX4_FEW_TOKENS)
+  if (W->kind == SOUP_WEIGHT_MXFP4 &&
+      (T <= MX4_FEW_TOKENS / 2 || (T <= MX4_FEW_TOKENS && W->out_features <= 16 * sm_count())))
     return mx4_few(W, x, ldx, (int)T, y, ldy, static_cast<cudaStream_t>(stream));
   if (W->kind == SOUP_WEIGHT_MXFP4 && T <= MX4_MID_TOKENS)
     return mx4_mid(W, false, x, ldx, (int)T, y, ldy, static_cast<cudaStream_t>(stream));

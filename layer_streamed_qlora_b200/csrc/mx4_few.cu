@@ -14,7 +14,7 @@
 // neighbouring codes of a thread, the first four and then the last four are
 // its four k of one instruction, and x is read in the same order.
 //
-// One token through 6144 x 4096 takes 8.1 us, through 28672 x 4096 24 us
+// One token through 6144 x 4096 takes 6.9 us, through 28672 x 4096 24 us
 // (2.6 TB/s): reading the codes in this pattern alone takes 4.1 and 10.4 us,
 // and the rest is the decode, some 36 instructions per 8 codes with the
 // integer pipe 60 % busy.  A table of byte pairs in shared memory halves the

@@ -26,8 +26,10 @@
 // decode left out 300 remain of the 490, and all of the 730: there the x tile
 // is the limit, 32 KB per k-block and SM from L2 (45 bytes a clock), and the
 // tensor core needs 512.  Weights in L2 instead of HBM make no difference.
-// 256 tokens through 28672 x 4096 take 57 us (1060 TFLOP/s), 64 take 45 us;
-// the GEMM engine's 256-token tiles take 84 us for either.
+// 256 tokens through 28672 x 4096 take 54 us (1110 TFLOP/s), 64 take 44 us;
+// the GEMM engine's 256-token tiles take 84 us for either.  The start of a
+// launch (barriers, tensor memory) runs while the kernel before it ends: 77
+// tokens backward through 2560 x 2016 14.0 -> 10.6 us.
 
 #include <cuda.h>
 
