@@ -32,6 +32,8 @@ class SoupError(RuntimeError):
 
 
 class SoupWeight(ctypes.Structure):
+    # index of the device that the buffers are on (-1: host memory), None where only addresses are known
+    device = None
     _fields_ = [("kind", c_int32), ("out_features", c_int64), ("in_features", c_int64),
                 ("codes", c_void_p), ("absmax", c_void_p), ("w", c_void_p), ("scales", c_void_p)]
 
@@ -45,6 +47,20 @@ class LayerCfg(ctypes.Structure):
 class LayerWeights(ctypes.Structure):
     _fields_ = [("qkv", SoupWeight), ("o", SoupWeight), ("gate_up", SoupWeight), ("down", SoupWeight),
                 ("norm1", c_void_p), ("norm2", c_void_p)]
+    device = None
+
+    def __init__(self, *args, **kwargs):
+        super().__init__(*args, **kwargs)
+        given = [w for w in (*args, *kwargs.values()) if isinstance(w, SoupWeight)]
+        self.device = _one_device("LayerWeights", [w.device for w in given])
+
+
+def _one_device(fn, devices):
+    """The device of all that is known of (None where nothing is)."""
+    known = {d for d in devices if d is not None}
+    if len(known) > 1:
+        raise ValueError(f"{fn}: buffers on different devices {sorted(known)} (-1: host memory)")
+    return known.pop() if known else None
 
 
 class LayerLora(ctypes.Structure):
@@ -353,6 +369,14 @@ def _device_of(fn, name, t):
     return dev
 
 
+def _w(fn, W):
+    """A weight (or a layer's) by reference, for a launch on the current CUDA device."""
+    if W.device is not None and (W.device < 0 or W.device != torch.cuda.current_device()):
+        where = "in host memory" if W.device < 0 else f"on device {W.device}"
+        raise ValueError(f"{fn}: the weight is {where}, not on the current CUDA device")
+    return ctypes.byref(W)
+
+
 def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
@@ -392,18 +416,28 @@ def soup_mx4_dequant(codes, scales, out_f, in_f, W_bf16, stream=None):
 
 
 # ---------------------------------------------------------------- weights
+# A weight may be described where there is no GPU; the calls that launch refuse
+# one that is not on the current device.
+def _weight(fn, w, *buffers) -> SoupWeight:
+    w.device = _one_device(fn, [t.get_device() for t in buffers])
+    return w
+
+
 def weight_nf4(codes, absmax, out_f, in_f) -> SoupWeight:
-    return SoupWeight(SOUP_WEIGHT_NF4, out_f, in_f, codes.data_ptr(), absmax.data_ptr(), None)
+    return _weight("weight_nf4", SoupWeight(SOUP_WEIGHT_NF4, out_f, in_f, codes.data_ptr(), absmax.data_ptr(), None),
+                   codes, absmax)
 
 
 def weight_bf16(w) -> SoupWeight:
-    return SoupWeight(SOUP_WEIGHT_BF16, w.shape[0], w.shape[1], None, None, w.data_ptr())
+    return _weight("weight_bf16", SoupWeight(SOUP_WEIGHT_BF16, w.shape[0], w.shape[1], None, None, w.data_ptr()), w)
 
 
 def weight_mxfp4(codes, scales, out_f, in_f) -> SoupWeight:
+    fn = "weight_mxfp4"
     for name, t, n in (("codes", codes, out_f * in_f // 2), ("scales", scales, out_f * soup_mx4_scale_stride(in_f))):
-        _ptr("weight_mxfp4", name, t, t.get_device(), torch.uint8, n)
-    return SoupWeight(SOUP_WEIGHT_MXFP4, out_f, in_f, codes.data_ptr(), None, None, scales.data_ptr())
+        _ptr(fn, name, t, t.get_device(), torch.uint8, n)
+    return _weight(fn, SoupWeight(SOUP_WEIGHT_MXFP4, out_f, in_f, codes.data_ptr(), None, None, scales.data_ptr()),
+                   codes, scales)
 
 
 # ---------------------------------------------------------------- frozen linear
@@ -419,7 +453,7 @@ def _linear(fn, f, W, x, x_cols, y, y_cols, workspace, stream):
     _device_of(fn, "input", x)
     ws = 0 if workspace is None else workspace.numel()
     wp = _ptr(fn, "workspace", workspace, dev, torch.uint8, 0) if ws else None
-    _check(fn, f(ctypes.byref(W), xp, ldx, T, yp, ldy, wp, ws, _raw_stream(stream, dev)))
+    _check(fn, f(_w(fn, W), xp, ldx, T, yp, ldy, wp, ws, _raw_stream(stream, dev)))
 
 
 def soup_linear_fwd(W: SoupWeight, x, y, workspace=None, stream=None):
@@ -490,8 +524,8 @@ class AdamWGroup:
 
 # ---------------------------------------------------------------- LoRA linear
 def soup_lora_linear_fwd(W: SoupWeight, A, B, r, scale, x, T, y, u_save, stream=None):
-    _check("soup_lora_linear_fwd", lib().soup_lora_linear_fwd(ctypes.byref(W), _p(A), _p(B), r, scale, _p(x), T,
-                                                              _p(y), _p(u_save), _stream(stream)))
+    _check("soup_lora_linear_fwd", lib().soup_lora_linear_fwd(
+        _w("soup_lora_linear_fwd", W), _p(A), _p(B), r, scale, _p(x), T, _p(y), _p(u_save), _stream(stream)))
 
 
 def soup_lora_linear_bwd_workspace(T, r, out_f) -> int:
@@ -500,7 +534,7 @@ def soup_lora_linear_bwd_workspace(T, r, out_f) -> int:
 
 def soup_lora_linear_bwd(W: SoupWeight, A, B, r, scale, x, u_save, dy, T, dx, dA, dB, workspace, stream=None):
     _check("soup_lora_linear_bwd", lib().soup_lora_linear_bwd(
-        ctypes.byref(W), _p(A), _p(B), r, scale, _p(x), _p(u_save), _p(dy), T, _p(dx), _p(dA), _p(dB),
+        _w("soup_lora_linear_bwd", W), _p(A), _p(B), r, scale, _p(x), _p(u_save), _p(dy), T, _p(dx), _p(dA), _p(dB),
         _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -511,7 +545,8 @@ def soup_lora_linear_bwd_noalloc_max_scratch() -> int:
 def soup_lora_linear_bwd_noalloc(W: SoupWeight, A, B, r, scale, x, u_save, dy, T, dx, dA, dB, stream=None):
     """soup_lora_linear_bwd without a workspace (static scratch; see soup.h)."""
     _check("soup_lora_linear_bwd_noalloc", lib().soup_lora_linear_bwd_noalloc(
-        ctypes.byref(W), _p(A), _p(B), r, scale, _p(x), _p(u_save), _p(dy), T, _p(dx), _p(dA), _p(dB),
+        _w("soup_lora_linear_bwd_noalloc", W),
+        _p(A), _p(B), r, scale, _p(x), _p(u_save), _p(dy), T, _p(dx), _p(dA), _p(dB),
         _stream(stream)))
 
 
@@ -539,7 +574,8 @@ def soup_decoder_layer_fwd(W: LayerWeights, lora, cfg: LayerCfg, h_in, batch, se
                            stream=None):
     lp = ctypes.byref(lora) if lora is not None else None
     _check("soup_decoder_layer_fwd", lib().soup_decoder_layer_fwd(
-        ctypes.byref(W), lp, ctypes.byref(cfg), _p(h_in), batch, seq, _p(h_out), int(adapters_on), _p(workspace),
+        _w("soup_decoder_layer_fwd", W),
+        lp, ctypes.byref(cfg), _p(h_in), batch, seq, _p(h_out), int(adapters_on), _p(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -548,7 +584,8 @@ def soup_decoder_layer_bwd(W: LayerWeights, lora, cfg: LayerCfg, h_in, dh_out, b
     lp = ctypes.byref(lora) if lora is not None else None
     gp = ctypes.byref(grads) if grads is not None else None
     _check("soup_decoder_layer_bwd", lib().soup_decoder_layer_bwd(
-        ctypes.byref(W), lp, ctypes.byref(cfg), _p(h_in), _p(dh_out), batch, seq, _p(dh_in), gp, int(adapters_on),
+        _w("soup_decoder_layer_bwd", W),
+        lp, ctypes.byref(cfg), _p(h_in), _p(dh_out), batch, seq, _p(dh_in), gp, int(adapters_on),
         _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -560,7 +597,8 @@ def soup_decoder_layer_fwd_keep(W: LayerWeights, lora, cfg: LayerCfg, h_in, batc
                                 workspace, stream=None):
     lp = ctypes.byref(lora) if lora is not None else None
     _check("soup_decoder_layer_fwd_keep", lib().soup_decoder_layer_fwd_keep(
-        ctypes.byref(W), lp, ctypes.byref(cfg), _p(h_in), batch, seq, _p(h_out), int(adapters_on), _p(qkv_keep),
+        _w("soup_decoder_layer_fwd_keep", W),
+        lp, ctypes.byref(cfg), _p(h_in), batch, seq, _p(h_out), int(adapters_on), _p(qkv_keep),
         _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -569,7 +607,8 @@ def soup_decoder_layer_bwd_kept(W: LayerWeights, lora, cfg: LayerCfg, h_in, dh_o
     lp = ctypes.byref(lora) if lora is not None else None
     gp = ctypes.byref(grads) if grads is not None else None
     _check("soup_decoder_layer_bwd_kept", lib().soup_decoder_layer_bwd_kept(
-        ctypes.byref(W), lp, ctypes.byref(cfg), _p(h_in), _p(dh_out), batch, seq, _p(dh_in), gp, int(adapters_on),
+        _w("soup_decoder_layer_bwd_kept", W),
+        lp, ctypes.byref(cfg), _p(h_in), _p(dh_out), batch, seq, _p(dh_in), gp, int(adapters_on),
         _p(qkv_kept), _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -581,7 +620,8 @@ def soup_decoder_layer_fwd_save(W: LayerWeights, lora, cfg: LayerCfg, h_in, batc
                                 workspace, stream=None):
     lp = ctypes.byref(lora) if lora is not None else None
     _check("soup_decoder_layer_fwd_save", lib().soup_decoder_layer_fwd_save(
-        ctypes.byref(W), lp, ctypes.byref(cfg), _p(h_in), batch, seq, _p(h_out), int(adapters_on), _p(saved),
+        _w("soup_decoder_layer_fwd_save", W),
+        lp, ctypes.byref(cfg), _p(h_in), batch, seq, _p(h_out), int(adapters_on), _p(saved),
         _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -590,7 +630,8 @@ def soup_decoder_layer_bwd_saved(W: LayerWeights, lora, cfg: LayerCfg, h_in, dh_
     lp = ctypes.byref(lora) if lora is not None else None
     gp = ctypes.byref(grads) if grads is not None else None
     _check("soup_decoder_layer_bwd_saved", lib().soup_decoder_layer_bwd_saved(
-        ctypes.byref(W), lp, ctypes.byref(cfg), _p(h_in), _p(dh_out), batch, seq, _p(dh_in), gp, int(adapters_on),
+        _w("soup_decoder_layer_bwd_saved", W),
+        lp, ctypes.byref(cfg), _p(h_in), _p(dh_out), batch, seq, _p(dh_in), gp, int(adapters_on),
         _p(saved), _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
