@@ -53,6 +53,7 @@ class LayerWeights(ctypes.Structure):
         super().__init__(*args, **kwargs)
         given = [w for w in (*args, *kwargs.values()) if isinstance(w, SoupWeight)]
         self.device = _one_device("LayerWeights", [w.device for w in given])
+        self.weights = given  # the structure holds copies of their addresses
 
 
 def _one_device(fn, devices):
@@ -416,10 +417,12 @@ def soup_mx4_dequant(codes, scales, out_f, in_f, W_bf16, stream=None):
 
 
 # ---------------------------------------------------------------- weights
-# A weight may be described where there is no GPU; the calls that launch refuse
-# one that is not on the current device.
+# A weight keeps its buffers alive (LayerWeights those of its weights).  It may
+# be described where there is no GPU; the calls that launch refuse one that is
+# not on the current device.
 def _weight(fn, w, *buffers) -> SoupWeight:
     w.device = _one_device(fn, [t.get_device() for t in buffers])
+    w.buffers = buffers
     return w
 
 

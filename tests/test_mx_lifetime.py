@@ -2,7 +2,9 @@
 live: checks of the binding that need no GPU (tensors that say they are on one
 stand in for its tensors, and no library call is made)."""
 import ctypes
+import gc
 import types
+import weakref
 
 import pytest
 import torch
@@ -100,3 +102,24 @@ def test_buffers_of_one_weight_or_layer_on_two_devices_are_refused(L):
     a, b = weights(L, cuda)[0], weights(L, lambda t: cuda(t, 1))[0]
     with pytest.raises(ValueError, match="different devices"):
         L.LayerWeights(a, a, b, a, None, None)
+
+
+@pytest.mark.parametrize("kind", range(3))
+@pytest.mark.parametrize("layer", [False, True])
+def test_weights_and_layers_keep_their_buffers(L, kind, layer):
+    """Buffers that only the weight was made from live as long as it, or the layer, does."""
+    made = []
+
+    def on(t):
+        made.append(weakref.ref(t.untyped_storage()))
+        return t
+
+    W = weights(L, on)
+    made = made[:2] if kind == 0 else made[2:4] if kind == 1 else made[4:]
+    keep = L.LayerWeights(W[kind], W[kind], W[kind], W[kind], None, None) if layer else W[kind]
+    del W
+    gc.collect()
+    assert all(r() is not None for r in made)
+    del keep
+    gc.collect()
+    assert not any(r() is not None for r in made)
