@@ -722,8 +722,9 @@ soup_status soup_adamw_step(float* theta, uint16_t* theta_bf16, float* grad, flo
  *
  * soup_adamw_group_init checks the tensors (SOUP_ERR_INVALID_ARG when two
  * buffers overlap), writes the group's tables to tables_dev
- * (soup_adamw_group_bytes, 16-byte aligned, kept by the caller while the group
- * is used), fills *group and SYNCHRONISES `stream`.  soup_adamw_group_step is
+ * (soup_adamw_group_bytes, 16-byte aligned, kept by the caller until the last
+ * step, or the last replay of a captured one, has run), fills *group and
+ * SYNCHRONISES `stream`.  soup_adamw_group_step is
  * one launch, asynchronous on `stream`; arguments as soup_adamw_step (t is
  * taken when the call is made: a captured step replays that t).  Steps of one
  * group must not overlap on the GPU. */

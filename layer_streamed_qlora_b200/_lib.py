@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 import torch
 
@@ -476,7 +477,10 @@ class AdamWGroup:
     tensors: dicts with theta (fp32), grad (fp32 or bf16, the same for all),
     m, v (fp32, or uint8 with m_scale, v_scale for state_bits=8) and optionally
     theta_bf16; all contiguous and on the current device.  The group keeps
-    them alive."""
+    them alive, with its own device tables; when it goes, their memory is used
+    again only behind the steps that were started, on whatever stream.  A step
+    captured into a graph reads them on every replay: keep the group for as
+    long as the graph."""
 
     def __init__(self, tensors, state_bits=32, stream=None):
         fn = "soup_adamw_group_init"
@@ -501,6 +505,7 @@ class AdamWGroup:
                 for k in ("m_scale", "v_scale"):
                     setattr(a, k, _ptr(fn, k, t.get(k), dev, torch.uint8, (n + 31) // 32) if n else None)
         self._tensors = tensors
+        self._streams = {}  # those of the steps, by handle
         self._handle = AdamWGroupHandle()
         nbytes = lib().soup_adamw_group_bytes(arr, len(tensors))
         self._dev = dev
@@ -519,10 +524,22 @@ class AdamWGroup:
         dev = torch.cuda.current_device()
         if self._dev != dev:
             raise ValueError(f"{fn}: the group is on device {self._dev}, not on the current CUDA device")
+        raw = _raw_stream(stream, dev)
+        if raw not in self._streams:
+            self._streams[raw] = stream if stream is not None else torch.cuda.current_stream()
         _check(fn, lib().soup_adamw_group_step(self._ref, lr, beta1, beta2, eps, weight_decay, grad_scale, int(t),
                                                int(seed) & 0xFFFFFFFF, 1 if zero_grad else 0,
-                                               _ptr(fn, "nonfinite", nonfinite, dev, torch.int32, 1),
-                                               _raw_stream(stream, dev)))
+                                               _ptr(fn, "nonfinite", nonfinite, dev, torch.int32, 1), raw))
+
+    def __del__(self):
+        if sys.is_finalizing():
+            return
+        for stream in getattr(self, "_streams", {}).values():
+            self._tables.record_stream(stream)
+            for d in self._tensors:
+                for k, _ in AdamWTensor._fields_[1:]:
+                    if d.get(k) is not None:
+                        d[k].record_stream(stream)
 
 
 # ---------------------------------------------------------------- LoRA linear

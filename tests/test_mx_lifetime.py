@@ -1,6 +1,7 @@
 """Where the buffers of weights and optimiser groups are, and how long they
 live: checks of the binding that need no GPU (tensors that say they are on one
 stand in for its tensors, and no library call is made)."""
+import contextlib
 import ctypes
 import gc
 import types
@@ -10,12 +11,18 @@ import pytest
 import torch
 
 
+recorded = {}  # buffers by the stream that their memory waits for
+
+
 class Cuda(torch.Tensor):
     """A host tensor that says it is on CUDA device `index`."""
     index = 0
 
     def get_device(self):
         return self.index
+
+    def record_stream(self, stream):
+        recorded.setdefault(stream, set()).add(self.data_ptr())
 
 
 def cuda(t, index=0):
@@ -39,7 +46,7 @@ def L(monkeypatch):
     monkeypatch.setattr(_lib, "_raw_stream", lambda stream, dev: 0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     ns = types.SimpleNamespace(**{k: getattr(_lib, k) for k in dir(_lib) if not k.startswith("__")})
-    ns.called = called
+    ns.called, ns.module = called, _lib
     return ns
 
 
@@ -123,3 +130,45 @@ def test_weights_and_layers_keep_their_buffers(L, kind, layer):
     del keep
     gc.collect()
     assert not any(r() is not None for r in made)
+
+
+def adamw_group(L, monkeypatch, **kw):
+    """A group of two tensors, the second without a bf16 copy, and the addresses of its buffers."""
+    recorded.clear()
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: cuda(empty(*a, **k)))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    f = lambda: cuda(torch.zeros(64))
+    parts = [dict(theta=f(), theta_bf16=cuda(torch.zeros(64, dtype=torch.bfloat16)), grad=f(), m=f(), v=f()),
+             dict(theta=f(), theta_bf16=None, grad=f(), m=f(), v=f(), name="second")]
+    group = L.AdamWGroup(parts, 32, **kw)
+    buffers = {t.data_ptr() for p in parts for t in p.values() if isinstance(t, torch.Tensor)}
+    return group, buffers | {group._tables.data_ptr()}
+
+
+HP = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=1.0, t=1)
+
+
+def test_a_group_that_goes_leaves_its_memory_to_the_streams_it_stepped_on(L, monkeypatch):
+    """The memory of the tables, and of tensors that nothing else holds, must not be handed out before steps on
+    other streams have read it."""
+    side = type("Side", (), {"cuda_stream": 77})()
+    now = type("Now", (), {"cuda_stream": 5})()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now)
+    monkeypatch.setattr(L.module, "_raw_stream", lambda stream, dev: 5 if stream is None else stream.cuda_stream)
+    group, buffers = adamw_group(L, monkeypatch)
+    for stream in (side, None, side, None):
+        group.step(**HP, stream=stream)
+    assert L.called.count("soup_adamw_group_step") == 4 and not recorded
+    del group
+    gc.collect()
+    assert recorded == {side: buffers, now: buffers}
+
+
+def test_a_group_that_never_stepped_or_failed_goes_quietly(L, monkeypatch):
+    group, _ = adamw_group(L, monkeypatch)
+    del group
+    with pytest.raises(ValueError, match="no tensors"):
+        L.AdamWGroup([])
+    gc.collect()
+    assert not recorded
