@@ -42,13 +42,12 @@ __device__ __forceinline__ void store_32B(void* p, const uint32_t (&w)[8], bool 
 // in 24.0 (6.2 TB/s; 28.8, and 26.6 without the early launch).  `dense`: scale rows have no
 // padding (in a multiple of 512), so a block's index is its scale's and no
 // division by the row length is needed; `packed` the same for W's rows.
+// W, codes and scales are read by ordinary loads: see dependent_launch.
 template <bool BF16>
-__global__ void __launch_bounds__(256) mx4_quantize_kernel(const void* __restrict__ W, int64_t units,
-                                                           uint32_t units_per_row, int64_t ldw,
-                                                           uint2* __restrict__ codes, uint8_t* __restrict__ scales,
-                                                           int64_t scale_stride, uint8_t* __restrict__ values,
-                                                           bool v32_in, bool v32_out, bool dense, bool packed,
-                                                           int32_t* __restrict__ nonfinite) {
+__global__ void __launch_bounds__(256)
+    mx4_quantize_kernel(const void* W, int64_t units, uint32_t units_per_row, int64_t ldw, uint2* codes,
+                        uint8_t* scales, int64_t scale_stride, uint8_t* values, bool v32_in, bool v32_out, bool dense,
+                        bool packed, int32_t* nonfinite) {
   ptx::grid_dep_wait();
   const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const bool in_range = u < units;  // the same for both halves of a block
@@ -112,14 +111,13 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const void* __restric
   }
 }
 
-__global__ void __launch_bounds__(256) mx4_dequant_kernel(const uint2* __restrict__ codes,
-                                                          const uint8_t* __restrict__ scales, int64_t units,
-                                                          uint32_t units_per_row, int64_t scale_stride,
-                                                          uint8_t* __restrict__ out, bool v32, bool dense) {
+__global__ void __launch_bounds__(256)
+    mx4_dequant_kernel(const uint2* codes, const uint8_t* scales, int64_t units, uint32_t units_per_row,
+                       int64_t scale_stride, uint8_t* out, bool v32, bool dense) {
   ptx::grid_dep_wait();
   const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (u >= units) return;
-  const uint2 c = __ldg(codes + u);
+  const uint2 c = codes[u];
   int64_t at = u >> 1;
   if (!dense) {
     const uint32_t row = (uint32_t)(u / units_per_row);
@@ -127,7 +125,7 @@ __global__ void __launch_bounds__(256) mx4_dequant_kernel(const uint2* __restric
   }
   const uint32_t w[2] = {c.x, c.y};
   uint32_t o[8];
-  mx4_decode<2>(w, __ldg(scales + at), o);
+  mx4_decode<2>(w, scales[at], o);
   store_32B(out + u * 32, o, v32);
 }
 

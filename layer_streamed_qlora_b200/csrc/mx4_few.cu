@@ -39,12 +39,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Loads of W and x are ordinary ones: see dependent_launch.
 // NT: groups of 8 tokens; DEPTH: turns whose loads of W are in flight together.
 template <int NT, int DEPTH>
-__global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 3 : 2) mx4_few_kernel(const uint8_t* __restrict__ codes,
-                                                               const uint8_t* __restrict__ scales, int N, int K,
-                                                               int64_t scale_stride, const uint16_t* __restrict__ x,
-                                                               int64_t ldx, int T, uint16_t* __restrict__ y, int64_t ldy) {
+__global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 3 : 2)
+    mx4_few_kernel(const uint8_t* codes, const uint8_t* scales, int N, int K, int64_t scale_stride, const uint16_t* x,
+                   int64_t ldx, int T, uint16_t* y, int64_t ldy) {
   __shared__ float part[WARPS][NT * 8][17];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
   const int row0 = blockIdx.x * 16, blocks = K / 32, turns = (blocks + 3) / 4;
@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 3 : 2) mx4_few_kernel(co
       for (int r = 0; r < 2; ++r) {
         const int row = row0 + 8 * r + g;
         const bool ok = b < blocks;
-        w[d][r] = ok ? __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)row * (K / 2)) + b) : make_uint4(0, 0, 0, 0);
-        s[d][r] = ok ? __ldg(scales + row * scale_stride + b) : 0u;
+        w[d][r] = ok ? reinterpret_cast<const uint4*>(codes + (int64_t)row * (K / 2))[b] : make_uint4(0, 0, 0, 0);
+        s[d][r] = ok ? scales[row * scale_stride + b] : 0u;
       }
     }
 #pragma unroll
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 ? 3 : 2) mx4_few_kernel(co
         for (int j = 0; j < NT; ++j) {
           const int t = 8 * j + g;
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (t < T && b < blocks) v = __ldg(reinterpret_cast<const uint4*>(x + t * ldx + (int64_t)b * 32) + u);
+          if (t < T && b < blocks) v = reinterpret_cast<const uint4*>(x + t * ldx + (int64_t)b * 32)[u];
           bx[j][0] = v.x;
           bx[j][1] = v.y;
           bx[j][2] = v.z;

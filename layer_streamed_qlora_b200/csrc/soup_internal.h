@@ -67,6 +67,11 @@ void profile_end(cudaStream_t st);
 // ends: its kernel calls ptx::grid_dep_wait before it touches memory, which
 // returns when that one has completed.  Set-up and launch latency are hidden
 // behind it (one attribute at attr[0]).
+// What the kernel before may have written is read by TMA or by ordinary loads
+// after the wait, never by non-coherent ones (__ldg, or what the compiler makes
+// of const __restrict__ parameters): those ask for data that nobody writes for
+// as long as the kernel runs, which now begins before that kernel's end, and
+// need not stay behind the wait.
 inline cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, size_t smem, cudaStream_t st,
                                            cudaLaunchAttribute* attr) {
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
