@@ -1036,9 +1036,11 @@ __global__ void __launch_bounds__(32 * (2 + (b_coded(BMD) ? 8 : 4)), 1)
         const uint8_t* src = args.codes + (size_t)kr * (args.N / 2) + (n0 + c0) / 2;
         const float* amp = args.absmax + (size_t)kr * (args.N / 64) + (n0 + c0) / 64;
         const size_t cstep = (size_t)BK * (args.N / 2), astep = (size_t)BK * (args.N / 64);
+        // N is a multiple of 64 and CPT divides 64: the columns are all inside or all beyond
+        const bool nvalid = n0 + c0 < args.N;
         uint32_t wn[NW];
         float amn = 0.f;
-        if (kr < args.K && num_kb > 0) {
+        if (nvalid && kr < args.K && num_kb > 0) {
           load_codes(src, wn);
           amn = __ldg(amp);
         }
@@ -1049,8 +1051,8 @@ __global__ void __launch_bounds__(32 * (2 + (b_coded(BMD) ? 8 : 4)), 1)
 #pragma unroll
           for (int u = 0; u < NW; ++u) w[u] = wn[u];
           const float am = amn;
-          const bool kvalid = it * BK + kr < args.K;
-          if (it + 1 < num_kb && (it + 1) * BK + kr < args.K) {
+          const bool valid = nvalid && it * BK + kr < args.K;
+          if (nvalid && it + 1 < num_kb && (it + 1) * BK + kr < args.K) {
             load_codes(src + (size_t)(it + 1) * cstep, wn);
             amn = __ldg(amp + (size_t)(it + 1) * astep);
           }
@@ -1065,7 +1067,7 @@ __global__ void __launch_bounds__(32 * (2 + (b_coded(BMD) ? 8 : 4)), 1)
             for (int u = 0; u < NW; ++u) {
               const int col = c0 + 8 * u;
               const int chunk = col >> 6, unit = (col >> 3) & 7;
-              const uint4 v = kvalid ? decode8(w[u], lut_lane, am) : make_uint4(0, 0, 0, 0);
+              const uint4 v = valid ? decode8(w[u], lut_lane, am) : make_uint4(0, 0, 0, 0);
               st_shared_v4(b + chunk * 8192 + kr * 128 + ((unit ^ (kr & 7)) << 4), v);
             }
             ptx::fence_proxy_async_smem();
