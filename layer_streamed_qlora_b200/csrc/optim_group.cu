@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(256, 4) adamw_group_kernel(const GroupArgs a) 
       v[i] = new_v(a, v[i], gi);
       // quotient and root to a few fp32 steps (2^-21 of the update in all): IEEE ones made the
       // 8-bit step bound by instructions, 197 instead of 165 us for 41.9 M parameters.  sqrt takes
-      // a subnormal v (root below 1.1e-19) as 0, which is 1e-7 of the least eps allowed on this path.
+      // a subnormal v (root below 1.1e-19) as 0: times inv_sqrt_bc2 that is 2^-23 of the least eps
+      // allowed on this path.
       const float q = a.tiny_eps ? __fdiv_rn(m[i], __fsqrt_rn(v[i]) * a.inv_sqrt_bc2 + a.eps)
                                  : m[i] * rcp_approx(fmaf(sqrt_approx(v[i]), a.inv_sqrt_bc2, a.eps));
       p[i] = fmaf(-a.step_size, q, p[i] * a.decay);
@@ -518,7 +519,7 @@ extern "C" soup_status soup_adamw_group_step(const soup_adamw_group* group, floa
   a.eps = eps;
   a.grad_scale = grad_scale;
   a.zero_grad = zero_grad ? 1 : 0;
-  a.tiny_eps = eps < 1e-12f;
+  a.tiny_eps = eps < 1e-12f * a.inv_sqrt_bc2;
   a.seed = seed;
   a.t = (uint32_t)t;
   a.nonfinite = nonfinite_dev;
