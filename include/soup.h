@@ -186,9 +186,11 @@ typedef struct soup_weight {
   int64_t out_features;  /* rows of W (N) */
   int64_t in_features;   /* columns of W (K); a multiple of 64 (MXFP4: of 32) */
   const uint8_t* codes;  /* NF4, MXFP4: [out, in/2] */
-  const float* absmax;   /* NF4: [out, in/64] */
+  union {                /* one place: the structure has the size that it had with NF4 and bf16 alone */
+    const float* absmax;   /* NF4: [out, in/64] */
+    const uint8_t* scales; /* MXFP4: [out, soup_mx4_scale_stride(in)] */
+  };
   const uint16_t* w;     /* BF16: [out, in] */
-  const uint8_t* scales; /* MXFP4: [out, soup_mx4_scale_stride(in)] */
 } soup_weight;
 
 /* Forward.  A [r, in] bf16, B [out, r] bf16 (r a multiple of 8, 8 <= r <= 64),

@@ -36,7 +36,17 @@ class SoupWeight(ctypes.Structure):
     # index of the device that the buffers are on (-1: host memory), None where only addresses are known
     device = None
     _fields_ = [("kind", c_int32), ("out_features", c_int64), ("in_features", c_int64),
-                ("codes", c_void_p), ("absmax", c_void_p), ("w", c_void_p), ("scales", c_void_p)]
+                ("codes", c_void_p), ("absmax", c_void_p), ("w", c_void_p)]
+
+    def __init__(self, kind=0, out_features=0, in_features=0, codes=None, absmax=None, w=None, scales=None):
+        if absmax is not None and scales is not None:
+            raise ValueError("SoupWeight: absmax (NF4) and scales (MXFP4) are one field")
+        super().__init__(kind, out_features, in_features, codes, absmax if scales is None else scales, w)
+
+    @property
+    def scales(self):
+        """MXFP4: where NF4 has absmax."""
+        return self.absmax
 
 
 class LayerCfg(ctypes.Structure):
