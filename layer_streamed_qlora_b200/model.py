@@ -32,6 +32,7 @@ from . import dp
 
 ITEM_EMBED, ITEM_HEAD = L.SOUP_ITEM_EMBED, L.SOUP_ITEM_HEAD
 PROJS = ("q", "k", "v", "o", "gate", "up", "down")
+_KINDS = {"nf4": L.SOUP_WEIGHT_NF4, "mxfp4": L.SOUP_WEIGHT_MXFP4, "bf16": L.SOUP_WEIGHT_BF16}
 
 
 @dataclass(frozen=True)
@@ -50,6 +51,10 @@ class ModelConfig:
     kind: str = "nf4"      # "nf4", "mxfp4" or "bf16" frozen base
     tied: bool = False     # lm_head == embed_tokens
 
+    def __post_init__(self):
+        if self.kind not in _KINDS:
+            raise ValueError(f"ModelConfig.kind must be one of {sorted(_KINDS)}, not {self.kind!r}")
+
     @property
     def qkv_out(self):
         return (self.n_q_heads + 2 * self.n_kv_heads) * self.head_dim
@@ -67,7 +72,7 @@ class ModelConfig:
 
     @property
     def weight_kind(self):
-        return {"nf4": L.SOUP_WEIGHT_NF4, "mxfp4": L.SOUP_WEIGHT_MXFP4}.get(self.kind, L.SOUP_WEIGHT_BF16)
+        return _KINDS[self.kind]
 
 
 def _seed(*parts) -> int:
