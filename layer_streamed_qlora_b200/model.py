@@ -397,6 +397,7 @@ class StreamedLoRAModel:
                 assert tuple(W.shape) == (sw.out_features, sw.in_features), (name, W.shape)
                 n = W.numel()
                 if kind == L.SOUP_WEIGHT_NF4:
+                    W = W.to("cuda", torch.float32)  # what the quantiser reads; MXFP4's also takes bf16
                     st_ = L.lib().soup_nf4_quantize(L.c_void_p(W.data_ptr()), sw.out_features, sw.in_features,
                                                     L.c_void_p(sw.codes), L.c_void_p(sw.absmax),
                                                     L.c_void_p(flag.data_ptr()), L.c_void_p(st.cuda_stream))
