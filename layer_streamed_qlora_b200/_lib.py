@@ -467,7 +467,8 @@ def _linear(fn, f, W, x, x_cols, y, y_cols, workspace, stream):
     _device_of(fn, "input", x)
     ws = 0 if workspace is None else workspace.numel()
     wp = _ptr(fn, "workspace", workspace, dev, torch.uint8, 0) if ws else None
-    _check(fn, f(_w(fn, W), xp, ldx, T, yp, ldy, wp, ws, _raw_stream(stream, dev)))
+    w = ctypes.byref(W) if W.device == dev else _w(fn, W)
+    _check(fn, f(w, xp, ldx, T, yp, ldy, wp, ws, _raw_stream(stream, dev)))
 
 
 def soup_linear_fwd(W: SoupWeight, x, y, workspace=None, stream=None):
