@@ -720,20 +720,16 @@ soup_status soup_adamw_step(float* theta, uint16_t* theta_bf16, float* grad, flo
  * although one step moves them by less than a code.  A v above zero keeps a
  * code above zero.  A state that is not finite is stored as NaN.  The block
  * scale puts the largest finite element of m in [2^7, 2^8) and of v in
- * [2^14, 2^15), or is 2^-127.
- *
- * theta's update m / (sqrt(v) / sqrt(1 - beta2^t) + eps): with 32-bit states
- * root and quotient are correctly rounded, with 8-bit states the update is
- * within 2^-20 of itself.
+ * [2^14, 2^15).
  *
  * soup_adamw_group_init checks the tensors (SOUP_ERR_INVALID_ARG when two
  * buffers overlap), writes the group's tables to tables_dev
  * (soup_adamw_group_bytes, 16-byte aligned, kept by the caller until the last
  * step, or the last replay of a captured one, has run), fills *group and
- * SYNCHRONISES `stream`.  soup_adamw_group_step is one launch, asynchronous on
- * `stream`; arguments as soup_adamw_step (t is taken when the call is made: a
- * captured step replays that t).  Steps of one group must not overlap on the
- * GPU. */
+ * SYNCHRONISES `stream`.  soup_adamw_group_step is
+ * one launch, asynchronous on `stream`; arguments as soup_adamw_step (t is
+ * taken when the call is made: a captured step replays that t).  Steps of one
+ * group must not overlap on the GPU. */
 typedef struct soup_adamw_tensor {
   int64_t n;
   float* theta;

@@ -2,17 +2,16 @@
 // MXFP8 (8-bit elements, one E8M0 scale byte per block of 32): E4M3 for m,
 // E5M2 for v, whose range is squared.
 //
-// The update is that of optim.cu, in fp32 with correctly rounded roots and
-// quotients (the two differ in which products and sums they fuse); 8-bit states
-// round those less exactly, see below.  With 8-bit states a step decodes m and
-// v of each element, forms the new ones in fp32, updates theta from these, and stores
-// them again, each rounded to one of its two neighbours at random with the
-// probability that keeps the mean.  Rounded to nearest neither would follow
-// its average: a step moves v by a part 1 - beta2 (1e-3) of itself and m by 1
-// - beta1 (0.1) of its distance from the gradient, while half a code step is 6
-// to 12 % of v and 3 to 6 % of m: v would never fall, and m would stop at two
-// thirds of a constant gradient.  A v above zero keeps at least the smallest
-// code, so m / sqrt(v) has no zero divisor that the fp32 state would not have.
+// The update is that of optim.cu.  With 8-bit states a step decodes m and v
+// of each element, forms the new ones in fp32, updates theta from these, and
+// stores them again, each rounded to one of its two neighbours at random with
+// the probability that keeps the mean.  Rounded to nearest neither would
+// follow its average: a step moves v by a part 1 - beta2 (1e-3) of itself and
+// m by 1 - beta1 (0.1) of its distance from the gradient, while half a code
+// step is 6 to 12 % of v and 3 to 6 % of m: v would never fall, and m would
+// stop at two thirds of a constant gradient.  A v above zero keeps at least
+// the smallest code, so m / sqrt(v) has no zero divisor that the fp32 state
+// would not have.
 // The block's scale brings the largest element to [2^7, 2^8) (E4M3) or
 // [2^14, 2^15) (E5M2), below the largest value even after rounding up;
 // elements of m down to 2^-17 and of v down to 2^-31 of it have a code.  An
@@ -129,7 +128,7 @@ __device__ __forceinline__ uint32_t pack_bytes(const uint32_t* c) {
   return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
 
-// Special-function approximations (subnormal arguments and results as 0), for 8-bit states.
+// Special-function approximations (subnormal arguments and results as 0).
 __device__ __forceinline__ float sqrt_approx(float x) {
   float y;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -284,15 +283,12 @@ __global__ void __launch_bounds__(256, 4) adamw_group_kernel(const GroupArgs a) 
       const float gi = g[i] * a.grad_scale;
       m[i] = new_m(a, m[i], gi);
       v[i] = new_v(a, v[i], gi);
-      // 32-bit states: root and quotient correctly rounded; the step waits for HBM and is no slower
-      // for it (41.9 M parameters 194 us with fp32 gradients, 197 with the form below; one layer's
-      // 1.3 M 6.5 against 6.0).  8-bit states: to a few fp32 steps (2^-21 of the update in all), since
-      // correctly rounded ones made the step bound by instructions, 197 instead of 165 us.  There sqrt
-      // takes a subnormal v (root below 1.1e-19) as 0: times inv_sqrt_bc2 that is 2^-23 of the least
-      // eps allowed on this path.
-      const bool exact = BITS == 32 || a.tiny_eps;
-      const float q = exact ? __fdiv_rn(m[i], fmaf(__fsqrt_rn(v[i]), a.inv_sqrt_bc2, a.eps))
-                            : m[i] * rcp_approx(fmaf(sqrt_approx(v[i]), a.inv_sqrt_bc2, a.eps));
+      // quotient and root to a few fp32 steps (2^-21 of the update in all): IEEE ones made the
+      // 8-bit step bound by instructions, 197 instead of 165 us for 41.9 M parameters.  sqrt takes
+      // a subnormal v (root below 1.1e-19) as 0: times inv_sqrt_bc2 that is 2^-23 of the least eps
+      // allowed on this path.
+      const float q = a.tiny_eps ? __fdiv_rn(m[i], __fsqrt_rn(v[i]) * a.inv_sqrt_bc2 + a.eps)
+                                 : m[i] * rcp_approx(fmaf(sqrt_approx(v[i]), a.inv_sqrt_bc2, a.eps));
       p[i] = fmaf(-a.step_size, q, p[i] * a.decay);
     }
     bad |= !finite(gtop);
