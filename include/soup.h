@@ -701,8 +701,8 @@ soup_status soup_adamw_step(float* theta, uint16_t* theta_bf16, float* grad, flo
                             void* stream);
 
 /* ---------------------------------------------------------- AdamW group ---
- * The same AdamW step over many tensors in one launch, with the optimiser
- * states in fp32 or in 8 bits (MXFP8 of the OCP Microscaling Formats
+ * The AdamW step of soup_adamw_step over many tensors in one launch, with the
+ * optimiser states in fp32 or in 8 bits (MXFP8 of the OCP Microscaling Formats
  * specification: 8-bit elements, one E8M0 scale byte per block of 32).
  *
  * soup_adamw_tensor: n elements; theta fp32 master copy; theta_bf16 the bf16
@@ -720,16 +720,20 @@ soup_status soup_adamw_step(float* theta, uint16_t* theta_bf16, float* grad, flo
  * although one step moves them by less than a code.  A v above zero keeps a
  * code above zero.  A state that is not finite is stored as NaN.  The block
  * scale puts the largest finite element of m in [2^7, 2^8) and of v in
- * [2^14, 2^15).
+ * [2^14, 2^15), or is 2^-127.
+ *
+ * theta's update, step m / (sqrt(v) / sqrt(1 - beta2^t) + eps) of the new m and
+ * v, is within 2^-21 of itself: soup_adamw_step, whose root and quotient are
+ * correctly rounded, gives other last bits.
  *
  * soup_adamw_group_init checks the tensors (SOUP_ERR_INVALID_ARG when two
  * buffers overlap), writes the group's tables to tables_dev
  * (soup_adamw_group_bytes, 16-byte aligned, kept by the caller until the last
  * step, or the last replay of a captured one, has run), fills *group and
- * SYNCHRONISES `stream`.  soup_adamw_group_step is
- * one launch, asynchronous on `stream`; arguments as soup_adamw_step (t is
- * taken when the call is made: a captured step replays that t).  Steps of one
- * group must not overlap on the GPU. */
+ * SYNCHRONISES `stream`.  soup_adamw_group_step is one launch, asynchronous on
+ * `stream`; arguments as soup_adamw_step (t is taken when the call is made: a
+ * captured step replays that t).  Steps of one group must not overlap on the
+ * GPU. */
 typedef struct soup_adamw_tensor {
   int64_t n;
   float* theta;

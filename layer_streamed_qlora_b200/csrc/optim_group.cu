@@ -2,7 +2,8 @@
 // MXFP8 (8-bit elements, one E8M0 scale byte per block of 32): E4M3 for m,
 // E5M2 for v, whose range is squared.
 //
-// The update is that of optim.cu.  With 8-bit states a step decodes m and v
+// The update has the formula of optim.cu, but its root and quotient are not
+// correctly rounded ones (see below).  With 8-bit states a step decodes m and v
 // of each element, forms the new ones in fp32, updates theta from these, and
 // stores them again, each rounded to one of its two neighbours at random with
 // the probability that keeps the mean.  Rounded to nearest neither would
@@ -283,10 +284,11 @@ __global__ void __launch_bounds__(256, 4) adamw_group_kernel(const GroupArgs a) 
       const float gi = g[i] * a.grad_scale;
       m[i] = new_m(a, m[i], gi);
       v[i] = new_v(a, v[i], gi);
-      // quotient and root to a few fp32 steps (2^-21 of the update in all): IEEE ones made the
-      // 8-bit step bound by instructions, 197 instead of 165 us for 41.9 M parameters.  sqrt takes
-      // a subnormal v (root below 1.1e-19) as 0: times inv_sqrt_bc2 that is 2^-23 of the least eps
-      // allowed on this path.
+      // quotient and root to a few fp32 steps (2^-21 of the update in all).  Correctly rounded ones
+      // made the 8-bit step bound by instructions, 197 instead of 165 us for 41.9 M parameters, and
+      // cost the 32-bit one 187 instead of 181 (flat buffers, bf16 gradients, back-to-back calls).
+      // sqrt takes a subnormal v (root below 1.1e-19) as 0: times inv_sqrt_bc2 that is 2^-23 of the
+      // least eps allowed on this path.
       const float q = a.tiny_eps ? __fdiv_rn(m[i], __fsqrt_rn(v[i]) * a.inv_sqrt_bc2 + a.eps)
                                  : m[i] * rcp_approx(fmaf(sqrt_approx(v[i]), a.inv_sqrt_bc2, a.eps));
       p[i] = fmaf(-a.step_size, q, p[i] * a.decay);

@@ -34,3 +34,20 @@ def test_first_step_with_small_gradients(bits, g, beta2, eps):
     bound = abs(want) * (droot / (root * c + f(eps)) + 2.0 ** -21 + 4 * 2.0 ** -24) + 2.0 ** -24 * abs(want)
     got = t["theta"].double().cpu().numpy()
     assert (np.abs(got - want) <= bound).all(), (got[0], want, np.abs(got - want).max() / bound)
+
+
+@pytest.mark.parametrize("eps", [1e-8, 1e-30])
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+def test_32_bit_update_is_within_its_bound(eps, grad):
+    """From theta = 0, theta is the documented update of the new m and v, which the step also returns, to 2^-21."""
+    from layer_streamed_qlora_b200 import _lib as L
+    n, t = 1 << 18, 9
+    rng = np.random.default_rng(0)
+    new = lambda std: torch.from_numpy((rng.standard_normal(n) * std).astype(np.float32)).cuda()
+    d = dict(theta=torch.zeros(n, device="cuda"), grad=new(1e-3).to(grad), m=new(1e-3), v=new(1e-3).square())
+    L.AdamWGroup([d], 32).step(3e-3, 0.9, 0.999, eps, 0.05, 1.0, t)
+    f = lambda x: float(np.float32(x))
+    m, v, got = (d[k].double().cpu().numpy() for k in ("m", "v", "theta"))
+    step, c = f(f(3e-3) / (1 - f(0.9) ** t)), f(1 / np.sqrt(1 - f(0.999) ** t))
+    want = -step * m / (np.sqrt(v) * c + f(eps))
+    assert (np.abs(got - want) <= 2.0 ** -21 * np.abs(want)).all()
