@@ -1117,8 +1117,10 @@ __global__ void __launch_bounds__(32 * (2 + (b_coded(BMD) ? 8 : 4)), 1)
 // quadrant).  The shared-memory ring, NF4 decode, tail K-block and epilogues
 // are those of gemm_kernel with CTA pairs; the stage counter runs on across
 // tiles and the NF4 decode table is built once.
-// 2048 x 28672 x 4096 with MXFP4 codes takes 372 us: 1290 TFLOP/s, 0.79 of the
-// rate that cuBLAS measures at 8192^3 in bf16.
+// 2048 x 28672 x 4096 with MXFP4 codes takes 370 us in short runs (1300 TFLOP/s,
+// 0.80 of what cuBLAS measures in short runs at 8192^3 in bf16) and 433 repeated
+// under the power cap (1110, 0.81 of cuBLAS's sustained rate).  896 tiles are 12
+// rounds of the 74 pairs and 8 tiles more, whose round runs nearly empty.
 constexpr int PERSIST_THREADS = 32 * 18;
 
 struct PairTile {

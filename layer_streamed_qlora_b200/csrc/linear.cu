@@ -5,19 +5,29 @@
 // NF4 and bf16 weights, and MXFP4 ones with many tokens, run on the GEMM
 // engine.  Its 256 x 256 tiles leave most of the GPU idle when T is small;
 // with a workspace the tiles that do not fill a round are cut along K (slices
-// of at least 40 k-blocks: at 16 a 2048 x 512 x 1024 product took 24.7 us in
-// slices and 11.8 whole), summed in slice order.
-// MXFP4 weights with fewer tokens have kernels of their own, both measured
-// against the engine at 6144 x 4096 (us):
-//   T           1     8     16    33    256   512   1024   2048
-//   mx4_few     7.8   8.2   16.1  19.9 (T = 32)
-//   mx4_mid     13.8  14    14.1  14.5  19.5  28.2  53
-//   engine      37    37    37    37    36.5  54.7  65     89
-// so mx4_few takes up to 8 tokens of the forward and mx4_mid up to 1024.  From
-// 9 to 16 tokens mx4_few needs twice the registers and instructions, and wins
-// only where each SM has one of its CTAs at most (16 rows each): 14.1 us
-// against 16.9 at 2048 x 11008, but 23 against 22 at 4096 x 14336 and 52
-// against 42 at 28672 x 4096.
+// of at least 40 k-blocks: with 16 a 2048 x 512 x 1024 product took 24.7 us in
+// slices and 11.8 whole, and 1280 x 6144 x 4096, which leaves 46 tiles, 81 and
+// 61), summed in slice order.  Products of 64 k-blocks are never cut then: the
+// 4 tiles that 2048 x 4096 x 14336 leaves, backward, cost a round of their own.
+// MXFP4 weights with fewer tokens have kernels of their own.  Forward, us in
+// graph replays over weights that L2 does not hold:
+//   6144 x 4096, T    1     8     16    33    64    256   512   768   1024  2048
+//   mx4_few           7.6   8.1   15.8
+//   mx4_mid           13.5  13.5  13.7  14.4  14.6  19.3  27.8  28.2  52.3  79.9
+//   engine            33.2        32.9  33.0  33.2  33.8  34.2  34.8  62.1  89.2
+//   28672 x 4096, T   1     8     16    33    64    256   512   768   1024  2048
+//   mx4_few           23.9  28.2  52.2
+//   mx4_mid           41.7  41.5  41.6  42.5  43.6  55.1  111   147   221   372
+//   engine            75.6        60.5  60.9  61.1  62.3  113   148   200   411
+// so mx4_few takes up to 8 tokens of the forward and mx4_mid up to 1024, where
+// the engine is ahead for the largest matrices alone (from 800 tokens of 28672
+// x 4096; backward 161 against 200 us at 768).  From 9 to 16 tokens mx4_few
+// needs twice the registers and instructions, and wins only where each SM has
+// one of its CTAs at most (16 rows each): at 16 tokens 13.5 us against 16.4 for
+// 2048 x 11008, but 23.0 against 20.6 for 4096 x 14336.  The input gradient has
+// mx4_mid from one token on (13.6 us at 6144 x 4096).
+// NF4 and bf16 weights have the engine's 256-token tiles at any T: one token
+// through 6144 x 4096 takes 39 and 33 us, where reading W takes 2.2 and 7.7.
 #include <algorithm>
 
 #include "gemm.h"

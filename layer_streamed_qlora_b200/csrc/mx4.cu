@@ -39,9 +39,10 @@ __device__ __forceinline__ void store_32B(void* p, const uint32_t (&w)[8], bool 
 // Both kernels are bound by HBM: one thread per 16 elements (half a block),
 // whose loads and stores are 8 to 64 bytes each.  28672 x 4096 fp32 quantise
 // in 112 us (6.9 TB/s; with 8 elements per thread 134), 4096 x 14336 dequantise
-// in 24.0 (6.2 TB/s; 28.8, and 26.6 without the early launch).  `dense`: scale rows have no
-// padding (in a multiple of 512), so a block's index is its scale's and no
-// division by the row length is needed; `packed` the same for W's rows.
+// in 24.0 (6.2 TB/s; 28.8, and 26.6 without the early launch).  `dense`: scale
+// rows have no padding (in a multiple of 512), so a block's index is its
+// scale's and no division by the row length is needed; `packed` the same for
+// W's rows.
 // W, codes and scales are read by ordinary loads: see dependent_launch.
 template <bool BF16>
 __global__ void __launch_bounds__(256)

@@ -14,11 +14,14 @@
 // neighbouring codes of a thread, the first four and then the last four are
 // its four k of one instruction, and x is read in the same order.
 //
-// One token through 6144 x 4096 takes 6.9 us, through 28672 x 4096 24 us
-// (2.6 TB/s): reading the codes in this pattern alone takes 4.1 and 10.4 us,
-// and the rest is the decode, some 36 instructions per 8 codes with the
-// integer pipe 60 % busy.  A table of byte pairs in shared memory halves the
-// instructions and gained nothing (8.3 and 29 us: its loads compete with x's).
+// One token through 6144 x 4096 takes 6.9 us from L2 and 7.6 from HBM, through
+// 28672 x 4096 24 us (2.6 TB/s): reading the codes in this pattern alone takes
+// 4.1 and 10.4 us.  The rest is the decode, some 36 instructions per 8 codes
+// (integer pipe 60 %, issue slots 68 % busy), and an uneven grid: with three
+// CTAs per SM, 1792 CTAs are 4.04 rounds of 444, and of the 384 of 6144 rows
+// some SMs get three and some two.  A table of byte pairs in shared memory
+// halves the instructions and gained nothing (8.3 and 29 us: its loads compete
+// with x's).
 #include <algorithm>
 
 #include "linear.h"

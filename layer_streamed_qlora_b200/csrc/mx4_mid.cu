@@ -18,7 +18,7 @@
 // addresses).  In the forward a thread's 64 values are one row of A, and go to
 // tensor memory as the A operand: neither the stores nor the MMA's reads of A
 // take shared memory's port then (256 tokens through 28672 x 4096: 65 -> 57
-// us).  In the backward they are parts of 64 rows, and go to the swizzled
+// us when it was changed, 55 now).  In the backward they are parts of 64 rows, and go to the swizzled
 // stage in shared memory.
 //
 // What bounds it (forward, one CTA per SM, cycles per k-block from the slope
@@ -26,10 +26,13 @@
 // decode left out 300 remain of the 490, and all of the 730: there the x tile
 // is the limit, 32 KB per k-block and SM from L2 (45 bytes a clock), and the
 // tensor core needs 512.  Weights in L2 instead of HBM make no difference.
-// 256 tokens through 28672 x 4096 take 54 us (1110 TFLOP/s), 64 take 44 us;
-// the GEMM engine's 256-token tiles take 84 us for either.  The start of a
-// launch (barriers, tensor memory) runs while the kernel before it ends: 77
-// tokens backward through 2560 x 2016 14.0 -> 10.6 us.
+// The slice count (1, 2 or 4) leaves SMs idle beside that: 48 row tiles (6144
+// rows) run on 96 of 148, 112 tiles on 112, and 224 take two rounds for 1.5.
+// 256 tokens through 28672 x 4096 take 55 us (1090 TFLOP/s), 64 take 44 us; the
+// GEMM engine's 256-token tiles take 62 us for either.  The start of a launch
+// (barriers, tensor memory) runs while the kernel before it ends: calls of 77
+// tokens backward through 2560 x 2016 14.0 -> 10.6 us apart, 7 of which the
+// host takes for a call.
 
 #include <cuda.h>
 

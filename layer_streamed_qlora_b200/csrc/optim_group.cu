@@ -199,10 +199,14 @@ __device__ __forceinline__ uint32_t block_top(const float (&x)[8], bool& odd) {
 
 // One thread per 8 elements of a chunk: 4 lanes share a block of 32, and all
 // of a tensor's arrays move in 8- to 32-byte accesses.  41.9 M parameters take
-// 150 us with 8-bit states (5.1 TB/s: 72 instructions per element keep 60 % of
-// the issue slots busy) and 182 us with fp32 states and bf16 gradients (6.5
-// TB/s, the copy rate); five CTAs per SM spill, and are slower (164, 199).  The elements beyond a
-// tensor's end (in its last chunk alone) count as zeros and are not stored.
+// 145 to 151 us with 8-bit states and fp32 gradients (5.0 to 5.2 TB/s: 72
+// instructions per element keep 60 % of the issue slots busy), 138 with bf16
+// gradients (the same instructions for fewer bytes), and 181 to 183 us with
+// fp32 states and bf16 gradients (6.4 TB/s, the copy rate); five CTAs per SM
+// spill, and are slower (164, 199).  1.3 M parameters (640 chunks) are a round
+// of the 592 resident CTAs and 48 CTAs more: 7.3 us from L2.  The elements
+// beyond a tensor's end (in its last chunk alone) count as zeros and are not
+// stored.
 template <int BITS, bool G16>
 __global__ void __launch_bounds__(256, 4) adamw_group_kernel(const GroupArgs a) {
   ptx::grid_dep_wait();
